@@ -36,11 +36,14 @@ MOE_OP_LOAD_BALANCE = 5
 MOE_OP_EP_RECV_LAYOUT = 6
 MOE_OP_GROUPED_FFN_FP8 = 7
 MOE_OP_ROUTE_PERMUTE_EP = 8
+MOE_OP_NORM_BACKWARD = 9
+MOE_OP_GROUPED_FFN_W4 = 10
 
 WORKSPACE_HEADER = 256
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 # exported symbol -> (restype, argtypes); the single source for the loader and the tests
@@ -78,6 +81,19 @@ SIGNATURES = {
     "moe_mxfp8_quantize_rows": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_mxfp8_quantize_weights": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_grouped_ffn_fp8": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_norm_in": (_I, [_P, _P, _I, _I, _F, _P, _P, _P]),
+    "moe_norm_in_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_norm_out": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _F, _F, _I, _I, _P, _P, _P, _P]),
+    "moe_norm_out_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _F, _I, _I, _P, _P, _P, _P, _SZ,
+                                   _P]),
+    "moe_ckpt8_pack": (_I, [_P, _I, _I, _P, _P, _P]),
+    "moe_ckpt8_dispatch": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_ckpt8_swiglu": (_I, [_P, _P, _I, _I, _P, _P, _P]),
+    "moe_ckpt8_combine_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_w4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_w4_pack_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_ffn_w4": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                                _P, _SZ, _P]),
     "moe_debug_check_status": (_I, [ctypes.POINTER(ctypes.c_int)]),
     "moe_read_device_status": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
     "moe_debug_wait_timeout": (_I, [_P, _I, _P]),
@@ -692,6 +708,330 @@ def moe_grouped_ffn_fp8(xp: torch.Tensor, offsets: torch.Tensor, wgu, wd, save_g
         _ptr(xp), _ptr(offsets), E, M, d, I, _ptr(gq), _ptr(gsf), _ptr(dq), _ptr(dsf), _ptr(y),
         _ptr(h), _ptr(gu), _ptr(ws), ws.numel(), _stream(dev)))
     return y, h, gu
+
+
+# ---------------------------------------------------------------- the block's norms
+def _shaped(t: Optional[torch.Tensor], dtype, shape, name: str, dev):
+    """_need for a tensor (or None) of a known shape on a known device."""
+    if t is None:
+        return
+    _need(t, dtype, len(shape), name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _need_ws(ws: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
+    if ws is None:
+        return new_workspace(nbytes, dev)
+    if not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    return ws
+
+
+def moe_norm_in(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, out=None):
+    """RMS norm before the block: (xn [T,d] bf16, rstd [T] fp32)."""
+    _need(x, torch.bfloat16, 2, "x")
+    T, d = x.shape
+    dev = x.device
+    _shaped(gain, torch.float32, (d,), "gain", dev)
+    if out is None:
+        out = (torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev))
+    else:
+        _shaped(out[0], torch.bfloat16, (T, d), "xn", dev)
+        _shaped(out[1], torch.float32, (T,), "rstd", dev)
+    xn, rstd = out
+    _check("moe_norm_in", load().moe_norm_in(_ptr(x), _ptr(gain), T, d, float(eps), _ptr(xn),
+                                             _ptr(rstd), _stream(dev)))
+    return xn, rstd
+
+
+def moe_norm_in_backward(dxn: torch.Tensor, x: torch.Tensor, gain: torch.Tensor,
+                         rstd: torch.Tensor, dres: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, out=None):
+    """Gradient of moe_norm_in plus the residual's dres: (dx [T,d] bf16, dgain [d] fp32)."""
+    _need(dxn, torch.bfloat16, 2, "dxn")
+    T, d = dxn.shape
+    dev = dxn.device
+    _shaped(x, torch.bfloat16, (T, d), "x", dev)
+    _shaped(gain, torch.float32, (d,), "gain", dev)
+    _shaped(rstd, torch.float32, (T,), "rstd", dev)
+    _shaped(dres, torch.bfloat16, (T, d), "dres", dev)
+    ws = _need_ws(ws, workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d) if ws is None else 0, dev)
+    if out is None:
+        out = (torch.empty_like(dxn), torch.empty(d, dtype=torch.float32, device=dev))
+    else:
+        _shaped(out[0], torch.bfloat16, (T, d), "dx", dev)
+        _shaped(out[1], torch.float32, (d,), "dgain", dev)
+    dx, dgain = out
+    _check("moe_norm_in_backward", load().moe_norm_in_backward(
+        _ptr(dxn), _ptr(x), _ptr(gain), _ptr(rstd), _ptr(dres), T, d, _ptr(dx), _ptr(dgain),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(dev)))
+    return dx, dgain
+
+
+def _gate_args(gate: Optional[torch.Tensor], span: Optional[int], T: int, d: int, dev):
+    """(span, columns) of a gate [ceil(T / span), 1 or d]; span None: T for one row, else 1."""
+    if gate is None:
+        return 1, 1
+    _need(gate, torch.float32, 2, "gate")
+    rows, cols = gate.shape
+    if span is None:
+        span = max(T, 1) if rows == 1 else 1
+    span = int(span)
+    if span < 1 or cols not in (1, d) or rows != -(-T // span) or gate.device != dev:
+        raise ValueError(f"gate must be [ceil({T} / span), 1 or {d}] on {dev}, got "
+                         f"{tuple(gate.shape)} with span {span}")
+    return span, cols
+
+
+def moe_norm_out(y: torch.Tensor, resid: torch.Tensor, gain: Optional[torch.Tensor] = None,
+                 topk_w: Optional[torch.Tensor] = None, inv_perm: Optional[torch.Tensor] = None,
+                 shared_y: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                 span: Optional[int] = None, scale: float = 1.0, eps: float = 1e-6,
+                 save: bool = True, out=None):
+    """resid + scale * gate * norm(combine(y)) in one launch; without a gain the norm is left
+    out. y [T*K,d] in expert order with inv_perm and topk_w, or a plain [T,d]. Returns
+    (out [T,d] bf16, zsum [T,d] bf16, rstd [T] fp32): zsum (the combined rows) and rstd are
+    what moe_norm_out_backward needs, None with save=False; rstd is None without a gain."""
+    _need(y, torch.bfloat16, 2, "y")
+    _need(resid, torch.bfloat16, 2, "resid")
+    T, d = resid.shape
+    dev = y.device
+    if y.shape[1] != d or (y.shape[0] % T if T else y.shape[0]):
+        raise ValueError(f"y must be [T*K, {d}] with T = {T}, got {tuple(y.shape)}")
+    K = y.shape[0] // T if T else 1
+    _shaped(resid, torch.bfloat16, (T, d), "resid", dev)
+    _shaped(gain, torch.float32, (d,), "gain", dev)
+    _shaped(topk_w, torch.float32, (T, K), "topk_w", dev)
+    _shaped(inv_perm, torch.int32, (T * K,), "inv_perm", dev)
+    _shaped(shared_y, torch.bfloat16, (T, d), "shared_y", dev)
+    span, cols = _gate_args(gate, span, T, d, dev)
+    if out is None:
+        out = (torch.empty_like(resid), torch.empty_like(resid) if save else None,
+               torch.empty(T, dtype=torch.float32, device=dev)
+               if save and gain is not None else None)
+    else:
+        _shaped(out[0], torch.bfloat16, (T, d), "out", dev)
+        _shaped(out[1], torch.bfloat16, (T, d), "zsum", dev)
+        _shaped(out[2], torch.float32, (T,), "rstd", dev)
+    o, zsum, rstd = out
+    _check("moe_norm_out", load().moe_norm_out(
+        _ptr(y), _ptr(topk_w), _ptr(inv_perm), K, _ptr(shared_y), _ptr(resid), _ptr(gain),
+        _ptr(gate), span, cols, float(scale), float(eps), T, d, _ptr(o), _ptr(zsum), _ptr(rstd),
+        _stream(dev)))
+    return o, zsum, rstd
+
+
+def moe_norm_out_backward(dout: torch.Tensor, zsum: torch.Tensor, rstd: Optional[torch.Tensor],
+                          gain: Optional[torch.Tensor] = None,
+                          gate: Optional[torch.Tensor] = None, span: Optional[int] = None,
+                          scale: float = 1.0, ws: Optional[torch.Tensor] = None, out=None):
+    """(dz [T,d] bf16, dgain [d] fp32 or None, dgate like gate or None); rstd is read with a
+    gain only."""
+    _need(dout, torch.bfloat16, 2, "dout")
+    T, d = dout.shape
+    dev = dout.device
+    _shaped(zsum, torch.bfloat16, (T, d), "zsum", dev)
+    _shaped(rstd, torch.float32, (T,), "rstd", dev)
+    _shaped(gain, torch.float32, (d,), "gain", dev)
+    if gain is not None and rstd is None:
+        raise ValueError("rstd is needed with a gain")
+    span, cols = _gate_args(gate, span, T, d, dev)
+    ws = _need_ws(ws, workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d) if ws is None else 0, dev)
+    if out is None:
+        out = (torch.empty_like(dout), None if gain is None else torch.empty_like(gain),
+               None if gate is None else torch.empty_like(gate))
+    else:
+        _shaped(out[0], torch.bfloat16, (T, d), "dz", dev)
+        _shaped(out[1], torch.float32, (d,), "dgain", dev)
+        _shaped(out[2], torch.float32, tuple(gate.shape) if gate is not None else (), "dgate", dev)
+    dz, dgain, dgate = out
+    _check("moe_norm_out_backward", load().moe_norm_out_backward(
+        _ptr(dout), _ptr(zsum), _ptr(rstd), _ptr(gain), _ptr(gate), span, cols, float(scale), T, d,
+        _ptr(dz), _ptr(dgain), _ptr(dgate), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(dev)))
+    return dz, dgain, dgate
+
+
+# ---------------------------------------------------------------- 8-bit checkpoints
+def _ckpt8_args(q: torch.Tensor, s: torch.Tensor):
+    _need(q, torch.int8, 2, "q")
+    _shaped(s, torch.bfloat16, (q.shape[0], -(-q.shape[1] // 32)), "s", q.device)
+    return q.shape[0], q.shape[1], q.device
+
+
+def moe_ckpt8_pack(x: torch.Tensor, out=None):
+    """8-bit checkpoint of x [M,N] bf16: (q [M,N] int8, s [M, ceil(N/32)] bf16)."""
+    _need(x, torch.bfloat16, 2, "x")
+    M, N = x.shape
+    dev = x.device
+    if out is None:
+        out = (torch.empty(M, N, dtype=torch.int8, device=dev),
+               torch.empty(M, -(-N // 32), dtype=torch.bfloat16, device=dev))
+    else:
+        _shaped(out[0], torch.int8, (M, N), "q", dev)
+        _ckpt8_args(*out)
+    q, s = out
+    _check("moe_ckpt8_pack", load().moe_ckpt8_pack(_ptr(x), M, N, _ptr(q), _ptr(s), _stream(dev)))
+    return q, s
+
+
+def moe_ckpt8_dispatch(q: torch.Tensor, s: torch.Tensor, inv_perm: Optional[torch.Tensor] = None,
+                       K: int = 1, out: Optional[torch.Tensor] = None):
+    """The dispatched rows xp [T*K,d] bf16 of a checkpointed x (K = 1 and no inv_perm: x)."""
+    T, d, dev = _ckpt8_args(q, s)
+    _shaped(inv_perm, torch.int32, (T * K,), "inv_perm", dev)
+    if out is None:
+        out = torch.empty(T * K, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _shaped(out, torch.bfloat16, (T * K, d), "xp", dev)
+    _check("moe_ckpt8_dispatch", load().moe_ckpt8_dispatch(
+        _ptr(q), _ptr(s), _ptr(inv_perm), T, int(K), d, _ptr(out), _stream(dev)))
+    return out
+
+
+def moe_ckpt8_swiglu(q: torch.Tensor, s: torch.Tensor, out=None):
+    """(gu [M,2I] bf16, h [M,I] bf16) of a checkpointed [G | U]."""
+    M, N, dev = _ckpt8_args(q, s)
+    if N % 2:
+        raise ValueError("q must hold [G | U]: an even number of columns")
+    I = N // 2
+    if out is None:
+        out = (torch.empty(M, N, dtype=torch.bfloat16, device=dev),
+               torch.empty(M, I, dtype=torch.bfloat16, device=dev))
+    else:
+        _shaped(out[0], torch.bfloat16, (M, N), "gu", dev)
+        _shaped(out[1], torch.bfloat16, (M, I), "h", dev)
+    gu, h = out
+    _check("moe_ckpt8_swiglu", load().moe_ckpt8_swiglu(_ptr(q), _ptr(s), M, I, _ptr(gu), _ptr(h),
+                                                       _stream(dev)))
+    return gu, h
+
+
+def moe_ckpt8_combine_backward(dout: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
+                               topk_w: torch.Tensor, inv_perm: torch.Tensor, out=None):
+    """moe_combine_backward with y as a checkpoint: (dy [TK,d] bf16, dtopk_w [T,K] fp32)."""
+    TK, d, dev = _ckpt8_args(q, s)
+    _need(topk_w, torch.float32, 2, "topk_w")
+    T, K = topk_w.shape
+    if T * K != TK or topk_w.device != dev:
+        raise ValueError(f"topk_w must hold {TK} weights on {dev}, got {tuple(topk_w.shape)}")
+    _shaped(dout, torch.bfloat16, (T, d), "dout", dev)
+    _shaped(inv_perm, torch.int32, (TK,), "inv_perm", dev)
+    if out is None:
+        out = (torch.empty(TK, d, dtype=torch.bfloat16, device=dev),
+               torch.empty(T, K, dtype=torch.float32, device=dev))
+    else:
+        _shaped(out[0], torch.bfloat16, (TK, d), "dy", dev)
+        _shaped(out[1], torch.float32, (T, K), "dtopk_w", dev)
+    dy, dw = out
+    _check("moe_ckpt8_combine_backward", load().moe_ckpt8_combine_backward(
+        _ptr(dout), _ptr(q), _ptr(s), _ptr(topk_w), _ptr(inv_perm), T, K, d, _ptr(dy), _ptr(dw),
+        _stream(dev)))
+    return dy, dw
+
+
+# ---------------------------------------------------------------- 4-bit experts
+def moe_w4_quantize_weights(w: torch.Tensor, group: int = 128, out=None):
+    """Plain 4-bit codes [E,N,K/2] uint8 and scales [E,N,K/group] bf16 of w [E,K,N] bf16."""
+    _need(w, torch.bfloat16, 3, "w")
+    E, K, N = w.shape
+    if group not in (32, 64, 128) or K % group or K % 64:
+        raise ValueError(f"K = {K} must be a multiple of 64 and of group (32, 64 or 128), "
+                         f"got {group}")
+    if out is None:
+        out = (torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device),
+               torch.empty(E, N, K // group, dtype=torch.bfloat16, device=w.device))
+    else:
+        _shaped(out[0], torch.uint8, (E, N, K // 2), "codes", w.device)
+        _shaped(out[1], torch.bfloat16, (E, N, K // group), "scales", w.device)
+    codes, scales = out
+    _check("moe_w4_quantize_weights", load().moe_w4_quantize_weights(
+        _ptr(w), E, K, N, int(group), _ptr(codes), _ptr(scales), _stream(w.device)))
+    return codes, scales
+
+
+def moe_w4_pack_weights(codes_a: torch.Tensor, scales_a: torch.Tensor,
+                        codes_b: Optional[torch.Tensor] = None,
+                        scales_b: Optional[torch.Tensor] = None, out=None):
+    """Plain 4-bit weights laid out for moe_grouped_ffn_w4: (tiles uint8 [E, tiles, K/64, 512],
+    scales bf16 [E, tiles, K/group, 16]); gate (a) and up (b) share tiles."""
+    _need(codes_a, torch.uint8, 3, "codes_a")
+    _need(scales_a, torch.bfloat16, 3, "scales_a")
+    E, N, K = codes_a.shape[0], codes_a.shape[1], 2 * codes_a.shape[2]
+    dev = codes_a.device
+    ng = scales_a.shape[2]
+    if ng < 1 or K % ng or K % 64 or K // ng not in (32, 64, 128):
+        raise ValueError(f"K = {K} in {ng} groups: K must be a multiple of 64, groups of 32, 64 "
+                         "or 128")
+    group = K // ng
+    _shaped(scales_a, torch.bfloat16, (E, N, ng), "scales_a", dev)
+    if (codes_b is None) != (scales_b is None):
+        raise ValueError("codes_b and scales_b go together")
+    _shaped(codes_b, torch.uint8, (E, N, K // 2), "codes_b", dev)
+    _shaped(scales_b, torch.bfloat16, (E, N, ng), "scales_b", dev)
+    per = 16 if codes_b is None else 8
+    if N % per:
+        raise ValueError(f"N = {N} must be a multiple of {per}")
+    if out is None:
+        out = (torch.empty(E, N // per, K // 64, 512, dtype=torch.uint8, device=dev),
+               torch.empty(E, N // per, ng, 16, dtype=torch.bfloat16, device=dev))
+    else:
+        _shaped(out[0], torch.uint8, (E, N // per, K // 64, 512), "tiles", dev)
+        _shaped(out[1], torch.bfloat16, (E, N // per, ng, 16), "scales", dev)
+    tiles, scales = out
+    _check("moe_w4_pack_weights", load().moe_w4_pack_weights(
+        _ptr(codes_a), _ptr(scales_a), _ptr(codes_b), _ptr(scales_b), E, N, K, group, _ptr(tiles),
+        _ptr(scales), _stream(dev)))
+    return tiles, scales
+
+
+def _w4_weight(w, E: int, per: int, name: str, dev):
+    """(outputs of one matrix, K, group) of laid-out weights with `per` of its outputs a tile."""
+    tiles, scales = w
+    _need(tiles, torch.uint8, 4, name + " tiles")
+    nt, kt = tiles.shape[1], tiles.shape[2]
+    ng = scales.shape[2] if scales.dim() == 4 else 0
+    if tiles.shape[0] != E or tiles.shape[3] != 512 or ng < 1 or (64 * kt) % ng:
+        raise ValueError(f"{name} must come from moe_w4_pack_weights for {E} experts")
+    _shaped(tiles, torch.uint8, tuple(tiles.shape), name + " tiles", dev)
+    _shaped(scales, torch.bfloat16, (E, nt, ng, 16), name + " scales", dev)
+    return nt * per, 64 * kt, 64 * kt // ng
+
+
+def moe_grouped_ffn_w4(x: torch.Tensor, offsets: torch.Tensor, wgu, wd,
+                       perm: Optional[torch.Tensor] = None, K: int = 1,
+                       ws: Optional[torch.Tensor] = None, out=None):
+    """SwiGLU experts on 4-bit weights: (y [M,d] bf16, h [M,I] bf16). ``wgu`` and ``wd`` come
+    from moe_w4_pack_weights (gate and up; down). With perm, x [T,d] are the tokens and row p
+    is x[perm[p] / K]; without, x [M,d] holds the rows in expert order."""
+    _need(x, torch.bfloat16, 2, "x")
+    _need(offsets, torch.int32, 1, "offsets")
+    T, d = x.shape
+    dev = x.device
+    E = offsets.numel() - 1
+    M = T * int(K) if perm is not None else T
+    _shaped(perm, torch.int32, (M,), "perm", dev)
+    I, k_gu, group_gu = _w4_weight(wgu, E, 8, "wgu", dev)
+    n_d, k_d, group_d = _w4_weight(wd, E, 16, "wd", dev)
+    if k_gu != d or n_d != d or k_d != I or offsets.device != dev:
+        raise ValueError(f"weights of [{k_gu} -> {I}] and [{k_d} -> {n_d}] do not fit x of {d}")
+    ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_FFN_W4, T, E, K, 1, d, I) if ws is None else 0,
+                  dev)
+    if out is None:
+        out = (torch.empty(M, d, dtype=torch.bfloat16, device=dev),
+               torch.empty(M, I, dtype=torch.bfloat16, device=dev))
+    else:
+        _shaped(out[0], torch.bfloat16, (M, d), "y", dev)
+        _shaped(out[1], torch.bfloat16, (M, I), "h", dev)
+    y, h = out
+    _check("moe_grouped_ffn_w4", load().moe_grouped_ffn_w4(
+        _ptr(x), _ptr(perm), T, int(K), _ptr(offsets), E, M, d, I, group_gu, group_d, _ptr(wgu[0]),
+        _ptr(wgu[1]), _ptr(wd[0]), _ptr(wd[1]), _ptr(y), _ptr(h), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(dev)))
+    return y, h
 
 
 def moe_profile_start(capacity: int = 4096):

@@ -12,6 +12,7 @@ size_t ffn_backward_scratch(long long M, int E, int d, int I);   // grouped_gemm
 size_t load_balance_workspace(int E);                       // route.cu
 size_t ffn_fp8_scratch(long long M, int E, int d, int I);   // grouped_gemm.cu
 size_t route_permute_workspace(long long TK, int E, int R);   // front.cu
+size_t norm_backward_workspace(int T, int d);               // norm.cu
 
 namespace {
 thread_local int g_last_cuda_error = 0;
@@ -103,6 +104,11 @@ extern "C" size_t moe_workspace_size(int op, int T, int E, int K, int R, int d, 
     case MOE_OP_GROUPED_FFN_FP8:
       if (I < 128 || d < 128 || d % 128 || I % 128) return 0;
       return kWorkspaceHeader + ffn_fp8_scratch(TK, E, d, I);
+    case MOE_OP_NORM_BACKWARD:
+      return norm_backward_workspace(T, d);
+    case MOE_OP_GROUPED_FFN_W4:
+      if (I < 64 || d < 64 || d % 64 || I % 64) return 0;
+      return kWorkspaceHeader;
     default:
       return 0;
   }
@@ -116,6 +122,9 @@ int debug_status_gather();
 int debug_status_ep();
 int debug_status_fp8();
 int debug_status_gemm();
+int debug_status_norm();
+int debug_status_ckpt8();
+int debug_status_w4();
 }  // namespace moe
 #endif
 
@@ -130,7 +139,8 @@ extern "C" int moe_debug_check_status(int* host_status) {
   }
   int first = 0;
   for (int v : {debug_status_route(), debug_status_permute(), debug_status_gather(),
-                debug_status_ep(), debug_status_fp8(), debug_status_gemm()}) {
+                debug_status_ep(), debug_status_fp8(), debug_status_gemm(), debug_status_norm(),
+                debug_status_ckpt8(), debug_status_w4()}) {
     if (v == MOE_ERR_CUDA) return MOE_ERR_CUDA;
     if (!first) first = v;
   }

@@ -72,7 +72,9 @@ enum moe_op {
   MOE_OP_LOAD_BALANCE = 5,
   MOE_OP_EP_RECV_LAYOUT = 6,
   MOE_OP_GROUPED_FFN_FP8 = 7,
-  MOE_OP_ROUTE_PERMUTE_EP = 8
+  MOE_OP_ROUTE_PERMUTE_EP = 8,
+  MOE_OP_NORM_BACKWARD = 9,
+  MOE_OP_GROUPED_FFN_W4 = 10
 };
 
 /* Bytes of device workspace the operation needs for these sizes (0 on bad
@@ -516,6 +518,139 @@ int moe_grouped_ffn_fp8(const moe_bf16* xp, const int32_t* offsets, int E, int M
                         const uint8_t* wgu_q, const uint8_t* wgu_sf, const uint8_t* wd_q,
                         const uint8_t* wd_sf, moe_bf16* y, moe_bf16* h, moe_bf16* gu, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The block around the layer: RMS norms before and after it, with the gate, the
+ * residual scale and the residual add. d % 8 == 0, d <= 16384; vectors and
+ * statistics are fp32. Results are the same bits on every run (fixed summation
+ * orders, no atomics).
+ * ------------------------------------------------------------------------ */
+
+/* Norm before the block: r_t = (mean_c x_tc^2 + eps)^(-1/2), xn = bf16(x r gain).
+ *   x [T,d] bf16 in, gain [d] fp32 in; xn [T,d] bf16 out, rstd [T] fp32 out (r,
+ *   for the gradient). eps >= 0. */
+int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, float eps, moe_bf16* xn,
+                float* rstd, void* stream);
+
+/* Gradient of moe_norm_in, joined with the residual stream's: with xh = x r and
+ * u = gain dxn,
+ *   dx = bf16(dres + r (u - xh mean_c(u xh))),  dgain = sum_t dxn xh.
+ *   dxn, x [T,d] bf16, gain [d], rstd [T] in; dres [T,d] bf16 or NULL (zero).
+ *   dx [T,d] bf16 out; dgain [d] fp32 out (written, zero when T == 0).
+ *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. */
+int moe_norm_in_backward(const moe_bf16* dxn, const moe_bf16* x, const float* gain,
+                         const float* rstd, const moe_bf16* dres, int T, int d, moe_bf16* dx,
+                         float* dgain, void* ws, size_t ws_bytes, void* stream);
+
+/* End of the block in one launch: moe_combine, the norm after the block, its
+ * gate, the residual scale and the residual add.
+ *   z_t = sum_{j<K} topk_w[t,j] y[inv_perm[t*K+j]] + shared_y[t]   (fp32, slot order)
+ *   out = bf16(resid + scale * gate * (z r gain)),  r_t = (mean_c z_tc^2 + eps)^(-1/2);
+ *   gain NULL: no norm, out = bf16(resid + scale * gate * z).
+ *   y [T*K,d] bf16; topk_w [T,K] fp32 or NULL (ones); inv_perm [T*K] int32 or NULL
+ *   (row t*K+j is row t*K+j); with K = 1 and both NULL, y is a plain [T,d] input.
+ *   shared_y [T,d] bf16 or NULL; resid [T,d] bf16; gain [d] fp32 or NULL.
+ *   gate fp32 [ceil(T / span), gate_cols] or NULL (ones); token t uses row
+ *   t / span, gate_cols is 1 or d: one gate per token (span = 1, one column), per
+ *   channel (span = T), or a vector per sequence (span = its tokens) are forms of it.
+ *   out [T,d] bf16; zsum [T,d] bf16 or NULL: bf16(z) kept for the gradient (the
+ *   norm itself takes the unrounded z); rstd [T] fp32 or NULL (written with a gain).
+ * 1 <= K <= 32, T*K < 2^31. out may be resid. */
+int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_t* inv_perm, int K,
+                 const moe_bf16* shared_y, const moe_bf16* resid, const float* gain,
+                 const float* gate, int span, int gate_cols, float scale, float eps, int T, int d,
+                 moe_bf16* out, moe_bf16* zsum, float* rstd, void* stream);
+
+/* Gradient of moe_norm_out with respect to z, the gain and the gate (the
+ * residual's is dout itself; y's, topk_w's and shared_y's follow from dz by
+ * moe_combine_backward). With zh = z r, n = zh gain and dn = scale gate dout:
+ *   dz = bf16(r (gain dn - zh mean_c(gain dn zh))),  dgain = sum_t dn zh,
+ *   dgate = scale sum_{t of its row} dout n, over the columns too when gate_cols
+ *   is 1; without a gain dz = bf16(dn) and n = z.
+ *   dout, zsum [T,d] bf16, rstd [T] (with a gain), gain, gate as in moe_norm_out.
+ *   dz [T,d] bf16 out; dgain [d] fp32 out (with a gain; zero when T == 0); dgate
+ *   [ceil(T / span), gate_cols] fp32 out (with a gate).
+ *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. */
+int moe_norm_out_backward(const moe_bf16* dout, const moe_bf16* zsum, const float* rstd,
+                          const float* gain, const float* gate, int span, int gate_cols,
+                          float scale, int T, int d, moe_bf16* dz, float* dgain, float* dgate,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits. A [M, N] array is kept as codes q [M, N] int8
+ * and scales s [M, ceil(N / 32)] bf16, one per 32 consecutive elements of a row
+ * (the last block of a row may be shorter):
+ *   s = max(max|v| / 127, 2^-110) rounded up to bf16, the maximum over the
+ *   block's finite values; q = rint(v * fl32(1 / s)) in [-127, 127]; q = -128 for
+ *   a value that is not finite. Restored: q s, NaN for -128 (so an overflow in
+ *   the forward still reaches the gradients). A value within s / 2 of bf16's
+ *   largest may be restored as infinity.
+ * N (d, 2 I) a multiple of 8.
+ * ------------------------------------------------------------------------ */
+int moe_ckpt8_pack(const moe_bf16* x, int M, int N, int8_t* q, moe_bf16* s, void* stream);
+
+/* moe_dispatch_scatter from a checkpoint of x: xp[inv_perm[t*K+j]] = bf16(restored
+ * row t), rows read once. inv_perm NULL: xp[t*K+j] (with K = 1 the plain restore).
+ *   q [T,d] int8, s [T, ceil(d/32)] bf16 in; xp [T*K,d] bf16 out. 1 <= K <= 32. */
+int moe_ckpt8_dispatch(const int8_t* q, const moe_bf16* s, const int32_t* inv_perm, int T, int K,
+                       int d, moe_bf16* xp, void* stream);
+
+/* What moe_grouped_ffn_backward needs, from a checkpoint of its [G | U] alone:
+ *   gu = bf16(restored), h = bf16(silu(G) * U) of the restored values.
+ *   q [M,2I] int8, s [M, ceil(2I/32)] bf16 in; gu [M,2I] bf16, h [M,I] bf16 out. */
+int moe_ckpt8_swiglu(const int8_t* q, const moe_bf16* s, int M, int I, moe_bf16* gu, moe_bf16* h,
+                     void* stream);
+
+/* moe_combine_backward with y kept as a checkpoint: dy[p] = bf16(topk_w[a] dout[t]),
+ * dtopk_w[a] = <dout[t], restored y[p]>, p = inv_perm[a], a = t*K + j.
+ *   q [TK,d] int8, s [TK, ceil(d/32)] bf16; other arguments as there. */
+int moe_ckpt8_combine_backward(const moe_bf16* dout, const int8_t* q, const moe_bf16* s,
+                               const float* topk_w, const int32_t* inv_perm, int T, int K, int d,
+                               moe_bf16* dy, float* dtopk_w, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Experts on 4-bit weights with group scales, for the few rows per expert of a
+ * decoding batch (any number of rows is accepted; from about 32 rows per expert
+ * on, the bf16 and MXFP8 experts are the faster calls):
+ *   w[n][k] = s[n][k / group] (code[n][k] - 8),  codes 0 .. 15, group 32, 64 or 128.
+ * A plain 4-bit checkpoint has K contiguous: codes [E, N, K/2] uint8 (element k in
+ * the low half of byte k / 2 for even k, in the high half for odd k) and scales
+ * [E, N, K/group] bf16. K % 64 == 0, K % group == 0.
+ * ------------------------------------------------------------------------ */
+
+/* Plain codes and scales of weights w [E, K, N] bf16 (N contiguous, as
+ * moe_grouped_ffn takes them; finite): s = max|w| of the group / 7 rounded up to
+ * bf16 (at least 2^-110), code = rint(w * fl32(1 / s)) + 8 in 1 .. 15. */
+int moe_w4_quantize_weights(const moe_bf16* w, int E, int K, int N, int group, uint8_t* codes,
+                            moe_bf16* scales, void* stream);
+
+/* Lays plain weights out for moe_grouped_ffn_w4 (once, when they are loaded): tiles
+ * of 16 outputs x 64 K in tensor-core order.
+ *   One matrix (the down projection, K = I, N = d): codes_b, scales_b NULL,
+ *   N % 16 == 0; tiles [E, N/16, K/64, 512] uint8, scales [E, N/16, K/group, 16] bf16.
+ *   Gate and up (codes_a, scales_a the gate's, codes_b, scales_b the up
+ *   projection's, K = d, N = I): N % 8 == 0; 8 outputs of each share a tile: tiles
+ *   [E, N/8, K/64, 512], scales [E, N/8, K/group, 16]. */
+int moe_w4_pack_weights(const uint8_t* codes_a, const moe_bf16* scales_a, const uint8_t* codes_b,
+                        const moe_bf16* scales_b, int E, int N, int K, int group, uint8_t* tiles,
+                        moe_bf16* scales, void* stream);
+
+/* Grouped SwiGLU experts on 4-bit weights: moe_grouped_ffn's h = bf16(silu(X Wg) *
+ * (X Wu)) and y = bf16(h Wd) with fp32 accumulation, the scales applied to fp32
+ * sums (no weight is rounded).
+ *   perm NULL: x [M,d] bf16 holds the rows in expert order (T == M, K unused).
+ *   perm [M] int32: row p is x[perm[p] / K] of x [T,d], M == T*K, which takes
+ *   moe_build_permutation's perm and saves the dispatch.
+ *   offsets [E+1] int32 as in moe_grouped_ffn. wgu, wgu_s and wd, wd_s from
+ *   moe_w4_pack_weights (group sizes group_gu and group_d).
+ *   y [M,d] bf16 out, h [M,I] bf16 out (needed by the down projection).
+ *   ws: moe_workspace_size(MOE_OP_GROUPED_FFN_W4, T, E, K, 1, d, I) bytes.
+ * d % 64 == 0, I % 64 == 0, E <= 1024. */
+int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T, int K,
+                       const int32_t* offsets, int E, int M, int d, int I, int group_gu,
+                       int group_d, const uint8_t* wgu, const moe_bf16* wgu_s, const uint8_t* wd,
+                       const moe_bf16* wd_s, moe_bf16* y, moe_bf16* h, void* ws, size_t ws_bytes,
+                       void* stream);
 
 /* Diagnostics: runs the bounded device-side wait that every mbarrier wait of
  * the GEMM kernels uses, on an mbarrier that nothing completes, with a limit of

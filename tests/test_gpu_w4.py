@@ -1,0 +1,170 @@
+"""GPU parity of the 4-bit experts with the CPU oracle.
+
+Codes and scales are bit-exact. h and y are bf16 roundings of fp32 sums of exact
+products: within half a bf16 ulp of the oracle plus 1e-3 of the tensor's RMS (y
+against the product of the stored h)."""
+import numpy as np
+import pytest
+import torch
+
+from grouped_gemm_moe_gb300 import binding as B
+from oracle import block as K
+from oracle import moe_oracle as O
+
+from _parity import assert_bf16_close, dev, ensure_built, f64, i64, to_dev
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_built()
+
+
+def _nibbles(codes):
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+
+
+def _matrix(rng, E, N, Kd, group):
+    """(codes 0 .. 15, scales) with every code and scales of different sizes."""
+    codes = rng.integers(0, 16, size=(E, N, Kd))
+    s = O.round_bf16((0.2 + rng.random((E, N, Kd // group))) * 0.02)
+    return codes, s
+
+
+def _plain(m):
+    return to_dev(_nibbles(m[0]), torch.uint8), to_dev(m[1], BF)
+
+
+def _experts(seed, E, d, I, g_gu, g_d):
+    rng = np.random.default_rng(seed)
+    mats = [_matrix(rng, E, I, d, g_gu), _matrix(rng, E, I, d, g_gu), _matrix(rng, E, d, I, g_d)]
+    wgu = B.moe_w4_pack_weights(*_plain(mats[0]), *_plain(mats[1]))
+    wd = B.moe_w4_pack_weights(*_plain(mats[2]))
+    return [K.w4_values(*m) for m in mats], wgu, wd
+
+
+def _check(x, offsets, vals, wgu, wd):
+    y, h = B.moe_grouped_ffn_w4(to_dev(x, BF), to_dev(offsets, I32), wgu, wd)
+    ry, rh = K.grouped_ffn_w4(x, offsets, *vals, h=f64(h))
+    assert_bf16_close(f64(h), rh, "h")
+    assert_bf16_close(f64(y), ry, "y")
+    return y, h
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("E,Kd,N", [(1, 128, 8), (3, 256, 40), (5, 640, 136)])
+def test_quantize(E, Kd, N, group):
+    w = O.round_bf16(np.random.default_rng([E, Kd, N]).normal(size=(E, Kd, N)) * 0.02)
+    w[0, :group, 0] = 0.0
+    codes, s = B.moe_w4_quantize_weights(to_dev(w, BF), group)
+    rq, rs = K.w4_quantize(w, group)
+    assert np.array_equal(f64(s), rs)
+    c = i64(codes)
+    assert np.array_equal(np.stack([c & 15, c >> 4], -1).reshape(rq.shape), rq)
+
+
+@pytest.mark.parametrize("E,d,I,g_gu,g_d,counts", [
+    (1, 64, 64, 64, 64, [1]),
+    (1, 64, 64, 32, 32, [8]),
+    (2, 128, 64, 128, 64, [0, 3]),
+    (4, 256, 320, 64, 32, [7, 0, 8, 9]),
+    (3, 2048, 768, 128, 128, [1, 1, 1]),
+    (3, 768, 1408, 32, 128, [16, 17, 31]),
+    (2, 192, 704, 64, 64, [32, 33]),
+    (3, 512, 256, 128, 32, [65, 0, 100]),
+    (40, 128, 128, 32, 64, [0] * 17 + [2] + [0] * 15 + [1] + [0] * 6),   # slots past a ballot
+    (2, 4096, 128, 128, 128, [5, 12]),
+])
+def test_ffn(E, d, I, g_gu, g_d, counts):
+    vals, wgu, wd = _experts([E, d, I], E, d, I, g_gu, g_d)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    x = O.round_bf16(np.random.default_rng(d).normal(size=(offsets[-1], d)))
+    _check(x, offsets, vals, wgu, wd)
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 4), (1, 4, 4), (3, 2, 16), (16, 6, 8), (64, 2, 8)])
+def test_rows_through_the_permutation(T, k, E):
+    """Tokens read through moe_build_permutation's perm: the dispatched call's bits."""
+    d, I = 256, 128
+    vals, wgu, wd = _experts([T, k], E, d, I, 64, 32)
+    rng = np.random.default_rng(T)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    x = to_dev(O.round_bf16(rng.normal(size=(T, d))), BF)
+    _, offsets, perm, _ = B.moe_build_permutation(to_dev(idx, I32), E)
+    y, h = B.moe_grouped_ffn_w4(x, offsets, wgu, wd, perm=perm, K=k)
+    xp = B.moe_dispatch(x, perm, k)
+    y2, h2 = _check(f64(xp), i64(offsets), vals, wgu, wd)
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def test_a_row_does_not_depend_on_the_batch_it_is_in():
+    """Rows of one expert in a batch of 40 against batches of the same size class."""
+    vals, wgu, wd = _experts(3, 1, 512, 256, 64, 64)
+    x = O.round_bf16(np.random.default_rng(3).normal(size=(40, 512)))
+    y, _ = _check(x, np.array([0, 40]), vals, wgu, wd)
+    x2 = x.copy()
+    x2[1:] = 0.0
+    y2, _ = B.moe_grouped_ffn_w4(to_dev(x2, BF), to_dev(np.array([0, 40]), I32), wgu, wd)
+    assert torch.equal(y[0], y2[0]) and (y2[1:] == 0).all()
+
+
+def test_quantized_bf16_weights_end_to_end():
+    """bf16 weights quantized and laid out here, against the oracle's own quantization of them."""
+    E, d, I = 2, 256, 192
+    rng = np.random.default_rng(0)
+    w = [O.round_bf16(rng.normal(size=(E, a, b)) * 0.05) for a, b in ((d, I), (d, I), (I, d))]
+    plain = [B.moe_w4_quantize_weights(to_dev(m, BF), 32) for m in w]
+    wgu = B.moe_w4_pack_weights(*plain[0], *plain[1])
+    wd = B.moe_w4_pack_weights(*plain[2])
+    vals = [K.w4_values(*K.w4_quantize(m, 32)) for m in w]
+    _check(O.round_bf16(rng.normal(size=(24, d))), np.array([0, 10, 24]), vals, wgu, wd)
+
+
+def test_not_finite_rows_stay_apart():
+    vals, wgu, wd = _experts(4, 2, 128, 128, 32, 32)
+    x = O.round_bf16(np.random.default_rng(4).normal(size=(12, 128)))
+    offsets = np.array([0, 5, 12])
+    y, _ = _check(x, offsets, vals, wgu, wd)
+    x[2, 3] = np.nan
+    x[9, 100] = np.inf
+    y2, _ = B.moe_grouped_ffn_w4(to_dev(x, BF), to_dev(offsets, I32), wgu, wd)
+    keep = [i for i in range(12) if i not in (2, 9)]
+    assert torch.equal(y[keep], y2[keep]) and y2[2].isnan().all()
+
+
+def test_no_rows():
+    _, wgu, wd = _experts(5, 3, 64, 64, 32, 32)
+    x = torch.empty(0, 64, dtype=BF, device=dev())
+    y, h = B.moe_grouped_ffn_w4(x, torch.zeros(4, dtype=I32, device=dev()), wgu, wd)
+    assert y.shape == (0, 64) and h.shape == (0, 64)
+
+
+def test_refusals():
+    _, wgu, wd = _experts(6, 2, 128, 64, 64, 64)
+    x = torch.zeros(4, 128, dtype=BF, device=dev())
+    off = torch.tensor([0, 2, 4], dtype=I32, device=dev())
+    with pytest.raises(ValueError):
+        B.moe_w4_quantize_weights(torch.zeros(1, 96, 8, dtype=BF, device=dev()), 32)   # K % 64
+    with pytest.raises(ValueError):
+        B.moe_w4_quantize_weights(torch.zeros(1, 128, 8, dtype=BF, device=dev()), 48)
+    codes = torch.zeros(1, 12, 64, dtype=torch.uint8, device=dev())
+    with pytest.raises(ValueError):
+        B.moe_w4_pack_weights(codes, torch.ones(1, 12, 2, dtype=BF, device=dev()))     # N % 16
+    with pytest.raises(ValueError):
+        B.moe_w4_pack_weights(codes, torch.ones(1, 12, 2, dtype=BF, device=dev()), codes, None)
+    with pytest.raises(ValueError):
+        B.moe_grouped_ffn_w4(x, off, wd, wgu)
+    with pytest.raises(ValueError):
+        B.moe_grouped_ffn_w4(x[:, :64].contiguous(), off, wgu, wd)
+    with pytest.raises(ValueError):
+        B.moe_grouped_ffn_w4(x, off[:2], wgu, wd)
+    with pytest.raises(ValueError):
+        B.moe_grouped_ffn_w4(x, off, wgu, wd, perm=torch.zeros(4, dtype=I32, device=dev()), K=2)
+    with pytest.raises(TypeError):
+        B.moe_grouped_ffn_w4(x.float(), off, wgu, wd)
+    with pytest.raises(B.MoEError) as e:
+        B.moe_grouped_ffn_w4(x, off, wgu, wd, ws=torch.zeros(16, dtype=torch.uint8, device=dev()))
+    assert e.value.status == B.MOE_ERR_WORKSPACE
