@@ -136,11 +136,12 @@ def load(path: str = LIB_PATH):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()   # the signatures convert integers
 
 
 def _stream(dev: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    # the current stream's handle without building a Stream object around it
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _check(name: str, rc: int):
@@ -713,7 +714,8 @@ def moe_grouped_ffn_fp8(xp: torch.Tensor, offsets: torch.Tensor, wgu, wd, save_g
 # ---------------------------------------------------------------- the block's norms
 def _shaped(t: Optional[torch.Tensor], dtype, shape, name: str, dev):
     """_need for a tensor (or None) of a known shape on a known device."""
-    if t is None:
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                     and t.device == dev and t.is_contiguous()):
         return
     _need(t, dtype, len(shape), name)
     if tuple(t.shape) != tuple(shape):

@@ -14,13 +14,17 @@
 //                    (summed over the columns too when the gate has one)
 //
 // Every kernel reads each row once and is bound by HBM. A row group of G
-// threads (whole warps) owns one row at a time, one 16-byte vector per thread
-// (V = 1 up to d = 8192, then 2), so a row stays in registers between its
-// sum and its result and the sum costs one block barrier (none when G = 32).
-// Short rows put several groups in a block. Column sums (dg, dgate) stay in the
-// threads' registers over a group's contiguous rows; groups write them once to
-// the workspace and a second launch adds them in a fixed order: no atomics, the
-// same bits every run.
+// threads (whole warps) owns one row at a time, V 16-byte vectors per thread,
+// so a row stays in registers between its sum and its result. The forward
+// kernels take narrow groups (V = 8 or 4: few threads wait for a row's sum, and
+// many rows are in flight) once there are rows to fill the SMs, and one
+// vector per thread before that, where the latency of a row counts. The
+// gradient kernels keep column sums (dg, dgate) in registers over a group's
+// contiguous rows, so they stay at one or two vectors per thread and get their
+// bytes in flight from a ring in shared memory that every thread fills
+// for itself (cp.async; a thread reads only what it copied, so no barrier
+// guards the ring). Groups write their column sums once to the workspace and a
+// second launch adds them in a fixed order: no atomics, the same bits every run.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,200 +32,452 @@
 namespace moe {
 namespace {
 
+#ifndef NI_CUT1
+#define NI_CUT1 128
+#endif
+#ifndef NI_CUT2
+#define NI_CUT2 256
+#endif
+#ifndef NB_CUT
+#define NB_CUT 32
+#endif
 constexpr int kMaxD = 16384;
-constexpr int kGroupTarget = 256;    // threads of a block of several short-row groups
 
-// How rows of nv vectors map to threads.
+// How rows of nv vectors map to threads: G threads per row group (a multiple of
+// 32), `groups` groups per block.
 struct RowPlan {
-  int G;        // threads per row group: a multiple of 32
-  int groups;   // row groups per block
-  int V;        // vectors per thread
+  int G, groups;
   int block() const { return G * groups; }
 };
 
-RowPlan plan_rows(int d) {
-  const int nv = d / 8;
+RowPlan plan_rows(int d, int V) {
+  const int per = (d / 8 + V - 1) / V;
   RowPlan p;
-  p.V = nv <= 1024 ? 1 : 2;
-  const int per = (nv + p.V - 1) / p.V;
   p.G = (per + 31) / 32 * 32;
-  p.groups = std::max(1, kGroupTarget / p.G);
+  p.groups = std::max(1, 256 / p.G);
   return p;
 }
 
-int resident(const RowPlan& p) { return std::max(1, 1024 / p.block()); }
+// Sums over row groups of G threads, in every thread of the group. The blocks
+// call sum() in step with a counting `phase`: the two halves of the buffer
+// alternate, so one barrier per sum is enough (a half is written again only
+// after the next sum's barrier). A group's warps own consecutive floats, padded
+// with zeros to whole float4s.
+struct GroupSum {
+  float* half0;
+  int warps4, first, slot;   // float4s of a group, its first one, this warp's float
+  __device__ GroupSum(float (&buf)[64], int G, int grp, int lane) : half0(buf) {
+    warps4 = (G / 32 + 3) / 4;
+    first = grp * warps4;
+    slot = first * 4 + lane / 32;
+    if (G > 32) {
+      if (threadIdx.x < 64) buf[threadIdx.x] = 0.f;
+      if (blockDim.x < 64 && threadIdx.x < 32) buf[32 + threadIdx.x] = 0.f;
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ float sum(float v, int G, int phase) const {
+    v = warp_sum(v);
+    if (G == 32) return v;
+    float* half = half0 + (phase & 1) * 32;
+    if ((threadIdx.x & 31) == 0) half[slot] = v;
+    __syncthreads();
+    const float4* h = reinterpret_cast<const float4*>(half) + first;
+    float4 a = h[0];
+    float s = (a.x + a.y) + (a.z + a.w);
+    for (int w = 1; w < warps4; ++w) {
+      a = h[w];
+      s += (a.x + a.y) + (a.z + a.w);
+    }
+    return s;
+  }
+};
 
-// Sum over the G threads of the caller's row group, in every thread. Blocks call
-// it in step; `red` holds 2 x 32 floats per block (the two halves alternate by
-// `phase`, so one barrier per call is enough: a half is written again only
-// after the next call's barrier).
-__device__ __forceinline__ float group_sum(float v, int G, float* red, int phase) {
-  v = warp_sum(v);
-  if (G == 32) return v;
-  float* half = red + (phase & 1) * 32;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) half[warp] = v;
-  __syncthreads();
-  const int nw = G >> 5, first = warp / nw * nw;
-  float s = 0.f;
-  for (int w = 0; w < nw; ++w) s += half[first + w];
-  return s;
+// norm_in's ring: 128 KB an SM, with 1024 threads on it up to two vectors a
+// thread and 512 from four on.
+constexpr int in_stages(int V) { return V == 1 ? 8 : 4; }
+constexpr int in_threads(int V) { return V <= 2 ? 1024 : 512; }
+
+constexpr int max_threads(int V) { return V == 1 ? 1024 : 256; }
+
+__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// xn = bf16(x r g), rows strided over the grid's groups; the next row's loads
-// are issued before this row's sum.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the N newest groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// xn = bf16(x r g) over a group's consecutive rows, kStages - 1 of them on their
+// way in shared memory. Each thread reads only the vectors it copied itself, so
+// the ring has no barrier of its own.
+template <int V>
+__global__ void __launch_bounds__(in_threads(V), 1)
+norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain, float eps,
+                    float inv_d, int T, int chunk, int nv, int G, uint4* __restrict__ xn,
+                    float* __restrict__ rstd) {
+  pdl_enter();
+  constexpr int kStages = in_stages(V);
+  extern __shared__ uint4 ring[];   // [stage][v][thread]
+  __shared__ __align__(16) float red[64];
+  const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
+  const GroupSum group(red, G, grp, lane);
+  const long long worker = static_cast<long long>(blockIdx.x) * (blockDim.x / G) + grp;
+  const int row0 = min(worker * chunk, static_cast<long long>(T));
+  const int row1 = min(static_cast<long long>(row0) + chunk, static_cast<long long>(T));
+  bool has[V];
+  float g[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    has[v] = lane + v * G < nv;
+    if (has[v]) load8f(gain + (lane + v * G) * 8, g[v]);
+  }
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  auto slot = [&](int stage, int v) {
+    return (stage * V + v) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+  };
+  auto issue = [&](int t, int stage) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool live = t < row1 && has[v];
+      copy16(base + 16 * slot(stage, v),
+             x + (live ? static_cast<long long>(t) * nv + lane + v * G : 0), live);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int st = 0; st + 1 < kStages; ++st) issue(row0 + st, st);
+  for (int i = 0; i < chunk; ++i) {   // every group of a block runs every step
+    const int t = row0 + i;
+    copies_wait<kStages - 2>();
+    issue(t + kStages - 1, (i + kStages - 1) % kStages);   // the slot of row t - 1, read by now
+    float f[V][8], s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      unpack8(ring[slot(i % kStages, v)], f[v]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s = fmaf(f[v][q], f[v][q], s);
+    }
+    s = group.sum(s, G, i);
+    if (t >= row1) continue;
+    const float r = rsqrtf(s * inv_d + eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!has[v]) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[v][q] = f[v][q] * r * g[v][q];
+      stg_v4(xn + static_cast<long long>(t) * nv + lane + v * G, pack8(f[v]));
+    }
+    if (lane == 0) rstd[t] = r;
+  }
+  copies_wait<0>();
+}
+
+// xn = bf16(x r g), one row per group, one vector per thread: the fewest steps
+// between a row's arrival and its result, for calls with fewer rows than SMs
+// can hold.
 template <int V>
 __global__ void __launch_bounds__(1024, 1)
 norm_in_kernel(const uint4* __restrict__ x, const float* __restrict__ gain, float eps, float inv_d,
-               long long T, int nv, int G, uint4* __restrict__ xn, float* __restrict__ rstd) {
+               int nv, uint4* __restrict__ xn, float* __restrict__ rstd) {
   pdl_enter();
-  __shared__ float red[64];
+  __shared__ __align__(16) float red[64];
+  const int G = blockDim.x;
+  const GroupSum group(red, G, 0, threadIdx.x);
+  const long long t = blockIdx.x;
+  uint4 raw[V];
+  float s = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = threadIdx.x + v * G;
+    raw[v] = c < nv ? ldg_nc_v4(x + t * nv + c) : make_uint4(0u, 0u, 0u, 0u);
+    float f[8];
+    unpack8(raw[v], f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s = fmaf(f[q], f[q], s);
+  }
+  const float r = rsqrtf(group.sum(s, G, 0) * inv_d + eps);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = threadIdx.x + v * G;
+    if (c >= nv) break;
+    float f[8], g[8];
+    unpack8(raw[v], f);
+    load8f(gain + c * 8, g);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] = f[q] * r * g[q];
+    stg_v4(xn + t * nv + c, pack8(f));
+  }
+  if (threadIdx.x == 0) rstd[t] = r;
+}
+
+// Combine, norm, gate, residual, one row per group. The gathered vectors of a
+// column are loaded KC at a time before they are added (slot order, fp32), as in
+// the combine of this library, and z is never rounded on its way into the norm;
+// only the copy saved for the gradient is bf16.
+template <int KC, int V>
+__global__ void __launch_bounds__(max_threads(V), V == 1 ? 1 : 2)
+norm_out_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
+                const int32_t* __restrict__ inv_perm, int K, const uint4* __restrict__ shared_y,
+                const uint4* resid, const float* __restrict__ gain,
+                const float* __restrict__ gate, unsigned span, int gate_cols, float scale,
+                float eps, float inv_d, int T, int nv, int G, uint4* out,
+                uint4* __restrict__ zsum, float* __restrict__ rstd) {
+  pdl_enter();
+  __shared__ __align__(16) float red[64];
   const int groups = blockDim.x / G;
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
-  const long long stride = static_cast<long long>(gridDim.x) * groups;
-  float g[V][8];
-  bool has[V];
+  const GroupSum group(red, G, grp, lane);
+  const long long t = static_cast<long long>(blockIdx.x) * groups + grp;
+  const bool live = t < T;
+  const long long slots = static_cast<long long>(T) * K;
+  float z[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[v][q] = 0.f;
+  if (live) {
+    for (int j0 = 0; j0 < K; j0 += KC) {
+      int32_t pos[KC];
+      float wj[KC];
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        const long long a = t * K + j0 + j;
+        pos[j] = -1;
+        if (j0 + j < K) {
+          pos[j] = inv_perm ? __ldg(inv_perm + a) : static_cast<int32_t>(a);
+          wj[j] = w ? __ldg(w + a) : 1.f;
+          if (!index_ok(pos[j] >= 0 && pos[j] < slots)) pos[j] = 0;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = lane + v * G;
+        if (c >= nv) break;
+        uint4 a[KC];
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (pos[j] >= 0) a[j] = ldg_nc_v4(y + static_cast<long long>(pos[j]) * nv + c);
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          if (pos[j] >= 0) {
+            float f[8];
+            unpack8(a[j], f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) z[v][q] = fmaf(wj[j], f[q], z[v][q]);
+          }
+        }
+      }
+    }
+  }
+  float s = 0.f;
+  uint4 res[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = lane + v * G;
-    has[v] = c < nv;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) g[v][q] = has[v] ? __ldg(gain + c * 8 + q) : 0.f;
-  }
-  uint4 cur[V];
-  auto load = [&](long long t, uint4 (&to)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      to[v] = (t < T && has[v]) ? ldg_nc_v4(x + t * nv + lane + v * G) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  const long long first = static_cast<long long>(blockIdx.x) * groups;
-  load(first + grp, cur);
-  int phase = 0;
-  for (long long t0 = first; t0 < T; t0 += stride, ++phase) {
-    const long long t = t0 + grp;
-    uint4 next[V];
-    load(t + stride, next);
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
+    if (!live || c >= nv) break;
+    res[v] = *reinterpret_cast<const uint4*>(resid + t * nv + c);   // may be out's own row
+    if (shared_y) {
       float f[8];
-      unpack8(cur[v], f);
+      unpack8(ldg_nc_v4(shared_y + t * nv + c), f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s = fmaf(f[q], f[q], s);
+      for (int q = 0; q < 8; ++q) z[v][q] += f[q];
     }
-    s = group_sum(s, G, red, phase);
-    const float r = rsqrtf(s * inv_d + eps);
-    if (t < T) {
+    if (zsum) stg_v4(zsum + t * nv + c, pack8(z[v]));
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!has[v]) continue;
-        float f[8];
-        unpack8(cur[v], f);
+    for (int q = 0; q < 8; ++q) s = fmaf(z[v][q], z[v][q], s);
+  }
+  float r = 1.f;
+  if (gain) r = rsqrtf(group.sum(s, G, 0) * inv_d + eps);
+  if (!live) return;
+  if (gain && rstd && lane == 0) rstd[t] = r;
+  const float* grow =
+      gate ? gate + static_cast<long long>(static_cast<unsigned>(t) / span) * gate_cols : nullptr;
+  const bool wide = grow && gate_cols != 1;
+  const float m = (grow && !wide) ? scale * __ldg(grow) : scale;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = f[q] * r * g[v][q];
-        stg_v4(xn + t * nv + lane + v * G, pack8(f));
-      }
-      if (lane == 0) rstd[t] = r;
+  for (int v = 0; v < V; ++v) {
+    const int c = lane + v * G;
+    if (c >= nv) break;
+    float f[8], g[8];
+    unpack8(res[v], f);
+    if (gain) {
+      load8f(gain + c * 8, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[v][q] = z[v][q] * r * g[q];
+    }
+    if (wide) {
+      load8f(grow + c * 8, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[v][q] *= g[q];
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) cur[v] = next[v];
+    for (int q = 0; q < 8; ++q) f[q] = fmaf(m, z[v][q], f[q]);
+    stg_v4(out + t * nv + c, pack8(f));
   }
 }
 
-// Combine, norm, gate, residual. The gathered vectors of a column are loaded KC at
-// a time before they are added (slot order, fp32), as in the combine of this library,
-// and z is never rounded on its way into the norm; only the copy saved for the
-// gradient is bf16.
-template <int KC, int V>
+// The same over a group's consecutive rows, one vector per thread: while a row is
+// combined and normed, the gathered vectors of the next S - 1 rows are on their way
+// into the thread's own slots of shared memory. Lane j of each warp looks up
+// slot j's row and weight a row before they are needed.
+template <int S>
 __global__ void __launch_bounds__(1024, 1)
-norm_out_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
-                const int32_t* __restrict__ inv_perm, int K, const uint4* __restrict__ shared_y,
-                const uint4* __restrict__ resid, const float* __restrict__ gain,
-                const float* __restrict__ gate, unsigned span, int gate_cols, float scale,
-                float eps, float inv_d, long long T, int nv, int G, uint4* __restrict__ out,
-                uint4* __restrict__ zsum, float* __restrict__ rstd) {
+norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
+                     const int32_t* __restrict__ inv_perm, int K,
+                     const uint4* __restrict__ shared_y, const uint4* resid,
+                     const float* __restrict__ gain, const float* __restrict__ gate, unsigned span,
+                     int gate_cols, float scale, float eps, float inv_d, int T, int chunk, int nv,
+                     int G, uint4* out, uint4* __restrict__ zsum, float* __restrict__ rstd) {
   pdl_enter();
-  __shared__ float red[64];
-  const int groups = blockDim.x / G;
+  extern __shared__ uint4 ring[];   // [stage][K slots, residual, shared][thread]
+  __shared__ __align__(16) float red[64];
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
-  const long long stride = static_cast<long long>(gridDim.x) * groups;
-  int phase = 0;
-  for (long long t0 = static_cast<long long>(blockIdx.x) * groups; t0 < T; t0 += stride, ++phase) {
-    const long long t = t0 + grp;
-    const bool live = t < T;
-    float z[V][8];
-    uint4 res[V];
-    float s = 0.f;
+  const GroupSum group(red, G, grp, lane);
+  const int wl = threadIdx.x & 31;
+  const long long worker = static_cast<long long>(blockIdx.x) * (blockDim.x / G) + grp;
+  const int row0 = min(worker * chunk, static_cast<long long>(T));
+  const int row1 = min(static_cast<long long>(row0) + chunk, static_cast<long long>(T));
+  const bool has = lane < nv;
+  const int arrays = K + 1 + (shared_y ? 1 : 0);
+  const long long slots = static_cast<long long>(T) * K;
+  float g[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = lane + v * G;
-      const bool has = live && c < nv;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) z[v][q] = 0.f;
-      res[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (has) {
-        uint4 sh = make_uint4(0u, 0u, 0u, 0u);
-        if (shared_y) sh = ldg_nc_v4(shared_y + t * nv + c);
-        res[v] = ldg_nc_v4(resid + t * nv + c);
-        for (int j0 = 0; j0 < K; j0 += KC) {
-          uint4 a[KC];
-#pragma unroll
-          for (int j = 0; j < KC; ++j) {
-            if (j0 + j < K) {
-              long long p = inv_perm ? __ldg(inv_perm + t * K + j0 + j) : t * K + j0 + j;
-              if (!index_ok(p >= 0 && p < T * K)) p = 0;
-              a[j] = ldg_nc_v4(y + p * nv + c);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < KC; ++j) {
-            if (j0 + j < K) {
-              const float wj = w ? __ldg(w + t * K + j0 + j) : 1.f;
-              float f[8];
-              unpack8(a[j], f);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) z[v][q] = fmaf(wj, f[q], z[v][q]);
-            }
-          }
-        }
-        if (shared_y) {
-          float f[8];
-          unpack8(sh, f);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) z[v][q] += f[q];
-        }
-        if (zsum) stg_v4(zsum + t * nv + c, pack8(z[v]));
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s = fmaf(z[v][q], z[v][q], s);
+  for (int q = 0; q < 8; ++q) g[q] = 1.f;
+  if (gain && has) load8f(gain + lane * 8, g);
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  auto at = [&](int stage, int array) {
+    return (stage * arrays + array) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+  };
+  auto look_up = [&](int t) {   // lane j: the packed row of slot j
+    if (t >= row1 || wl >= K) return 0;
+    const long long a = static_cast<long long>(t) * K + wl;
+    const int p = inv_perm ? __ldg(inv_perm + a) : static_cast<int>(a);
+    return index_ok(p >= 0 && p < slots) ? p : 0;
+  };
+  auto weight = [&](int t) {
+    return (w && t < row1 && wl < K) ? __ldg(w + static_cast<long long>(t) * K + wl) : 1.f;
+  };
+  auto issue = [&](int t, int stage, int pos) {
+    const bool live = t < row1 && has;
+    for (int j = 0; j < K; ++j) {
+      const long long p = __shfl_sync(0xffffffffu, pos, j);
+      copy16(base + 16 * at(stage, j), y + (live ? p * nv + lane : 0), live);
     }
+    const long long own = live ? static_cast<long long>(t) * nv + lane : 0;
+    copy16(base + 16 * at(stage, K), resid + own, live);
+    if (shared_y) copy16(base + 16 * at(stage, K + 1), shared_y + own, live);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int st = 0; st + 1 < S; ++st) issue(row0 + st, st, look_up(row0 + st));
+  int pos = look_up(row0 + S - 1);
+  float wt = weight(row0);
+  for (int i = 0; i < chunk; ++i) {   // every group of a block runs every step
+    const int t = row0 + i;
+    const bool live = t < row1;
+    copies_wait<S - 2>();
+    issue(t + S - 1, (i + S - 1) % S, pos);   // the slots of row t - 1, read by now
+    pos = look_up(t + S);
+    const float next_wt = weight(t + 1);
+    const int stage = i % S;
+    float z[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < K; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, wt, j);
+      float f[8];
+      unpack8(ring[at(stage, j)], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] = fmaf(wj, f[q], z[q]);
+    }
+    if (shared_y) {
+      float f[8];
+      unpack8(ring[at(stage, K + 1)], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] += f[q];
+    }
+    const long long own = static_cast<long long>(t) * nv + lane;
+    if (zsum && live && has) stg_v4(zsum + own, pack8(z));
     float r = 1.f;
     if (gain) {
-      r = rsqrtf(group_sum(s, G, red, phase) * inv_d + eps);
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s = fmaf(z[q], z[q], s);
+      r = rsqrtf(group.sum(s, G, i) * inv_d + eps);
       if (rstd && live && lane == 0) rstd[t] = r;
     }
-    if (!live) continue;
-    const float* grow =
-        gate ? gate + static_cast<long long>(static_cast<unsigned>(t) / span) * gate_cols : nullptr;
-    const float row_scale = (grow && gate_cols == 1) ? scale * __ldg(grow) : scale;
+    if (live && has) {
+      float f[8], gt[8], m = scale * r;
+      unpack8(ring[at(stage, K)], f);
+      const float* grow =
+          gate ? gate + static_cast<long long>(static_cast<unsigned>(t) / span) * gate_cols : nullptr;
+      if (grow && gate_cols != 1) {
+        load8f(grow + lane * 8, gt);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = lane + v * G;
-      if (c >= nv) continue;
-      float f[8];
-      unpack8(res[v], f);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float n = z[v][q] * r;
-        if (gain) n *= __ldg(gain + c * 8 + q);
-        float m = row_scale;
-        if (grow && gate_cols != 1) m *= __ldg(grow + c * 8 + q);
-        f[q] = fmaf(m, n, f[q]);
+        for (int q = 0; q < 8; ++q) z[q] *= gt[q];
+      } else if (grow) {
+        m *= __ldg(grow);
       }
-      stg_v4(out + t * nv + c, pack8(f));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = fmaf(m, z[q] * g[q], f[q]);
+      stg_v4(out + own, pack8(f));
     }
+    wt = next_wt;
   }
+  copies_wait<0>();
 }
+
+// Shared memory of an SM and what a block of it costs beside its own, for the
+// ring kernels' residency.
+constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024, kSmemPerBlock = 227 * 1024;
+
+// Row groups of a kernel that walks consecutive rows: `resident` blocks per SM.
+struct ChunkPlan {
+  int grid, chunk, workers;
+};
+
+ChunkPlan plan_chunks(int T, const RowPlan& p, int resident) {
+  const long long most = static_cast<long long>(num_sms()) * resident * p.groups;
+  ChunkPlan c;
+  c.chunk = static_cast<int>(std::max(1LL, (T + most - 1) / most));
+  c.workers = (T + c.chunk - 1) / c.chunk;
+  c.grid = (c.workers + p.groups - 1) / p.groups;
+  return c;
+}
+
+// Launches a kernel that takes `smem` bytes of dynamic shared memory; the limit
+// is raised once per kernel and device.
+template <typename... KArgs, typename... Args>
+int launch_big(void (*kern)(KArgs...), int& configured, int grid, int block, size_t smem,
+               cudaStream_t st, const Args&... args) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 1024);
+    if (e != cudaSuccess) {
+      set_last_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    configured = dev;
+  }
+  return launch_pdl(kern, grid, block, smem, st, 1, args...);
+}
+
+// Calls with few rows take a block per row.
+bool few_rows(int T) { return T <= 2 * num_sms(); }
 
 // ----------------------------------------------------------------- gradients
 // A row group takes `chunk` consecutive rows. Its column sums go to slot arrays
@@ -244,7 +500,7 @@ struct BackwardArgs {
   float* part_gate0;
   float* part_gate1;
   float* row_dot;         // per-row gate gradients (gate of one column)
-  long long T, span, chunk;
+  int T, span, chunk;
   float scale, inv_d;
   int nv, G;
 };
@@ -255,133 +511,159 @@ __device__ __forceinline__ void store_cols(float* to, const float (&v)[8]) {
   p[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-template <int V, bool NORM, int GATE>
-__global__ void __launch_bounds__(1024, 1) norm_backward_kernel(BackwardArgs A) {
+// The ring: up to 192 KB an SM, four stages of three arrays with 1024 / V threads
+// on it (two stages and 512 threads with four vectors, where d > 8192).
+constexpr int ring_stages(int V) { return V <= 2 ? 4 : 2; }
+constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
+
+// With a = dout (or dxn), b = z (or x) and k = gain (times the gate's row and
+// scale where the gate has d columns, those being constant over a span), a row
+// costs three operations an element before its sum and three after:
+//   q = a b,  s = sum_c q k,  mean_c(u xh) = s r sg / d
+//   dz = (r sg) k a - (r r mean) b
+// where sg is the row's scalar, scale times its one-column gate. The column sums
+// are dg += q (r sg), or with a gate of d columns e += q r, from which both
+// dgate = scale gain e and dg += scale gate e follow when the span ends.
+template <int V, bool RES, bool NORM, int GATE>
+__global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(BackwardArgs A) {
   pdl_enter();
-  __shared__ float red[64];
-  const int G = A.G, nv = A.nv;
-  const int groups = blockDim.x / G;
+  constexpr int kStages = ring_stages(V), kArrays = RES ? 3 : 2;
+  constexpr bool kVec = GATE == kGateVector;
+  extern __shared__ uint4 ring[];   // [stage][array][v][thread]
+  __shared__ __align__(16) float red[64];
+  const int G = A.G, nv = A.nv, nthreads = blockDim.x;
+  const int groups = nthreads / G;
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
-  const long long worker = static_cast<long long>(blockIdx.x) * groups + grp;
-  const long long row0 = worker * A.chunk;
-  const long long row1 = row0 + A.chunk < A.T ? row0 + A.chunk : A.T;
-  float g[V][8], gt[V][8], dg[V][8], dgt[V][8];
+  const GroupSum group(red, G, grp, lane);
+  const int worker = blockIdx.x * groups + grp;
+  const int row0 = min(static_cast<long long>(worker) * A.chunk, static_cast<long long>(A.T));
+  const int row1 = min(static_cast<long long>(row0) + A.chunk, static_cast<long long>(A.T));
   bool has[V];
+  float k[V][8], dg[V][8], e[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = lane + v * G;
-    has[v] = c < nv;
+    has[v] = lane + v * G < nv;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      g[v][q] = (NORM && has[v]) ? __ldg(A.gain + c * 8 + q) : 1.f;
-      gt[v][q] = 1.f;
+      k[v][q] = 1.f;
       dg[v][q] = 0.f;
-      dgt[v][q] = 0.f;
+      e[v][q] = 0.f;
     }
+    if (NORM && !kVec && has[v]) load8f(A.gain + (lane + v * G) * 8, k[v]);
   }
-  uint4 cu[V], cx[V], cr[V];
-  float rs = 1.f, gs = 1.f;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto load = [&](long long t, uint4 (&u)[V], uint4 (&x)[V], uint4 (&res)[V], float& r, float& gsc) {
-    const bool live = t < row1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const long long at = t * nv + lane + v * G;
-      u[v] = (live && has[v]) ? ldg_nc_v4(A.up + at) : zero;
-      x[v] = (live && has[v]) ? ldg_nc_v4(A.x + at) : zero;
-      res[v] = (A.dres && live && has[v]) ? ldg_nc_v4(A.dres + at) : zero;
-    }
-    r = (NORM && live) ? __ldg(A.rstd + t) : 0.f;
-    gsc = (GATE == kGateScalar && live) ? __ldg(A.gate + static_cast<unsigned>(t) / static_cast<unsigned>(A.span)) : 1.f;
+  auto slot = [&](int stage, int array, int v) {
+    return ((stage * kArrays + array) * V + v) * nthreads + static_cast<int>(threadIdx.x);
   };
-  load(row0, cu, cx, cr, rs, gs);
-  long long span_id = -1, span_end = 0;
-  for (long long i = 0; i < A.chunk; ++i) {   // every group of a block runs every step
-    const long long t = row0 + i;
-    const bool live = t < row1;
-    uint4 nu[V], nx[V], nr[V];
-    float nrs, ngs;
-    load(t + 1, nu, nx, nr, nrs, ngs);
-    if (GATE == kGateVector && live && t >= span_end) {   // a span begins (or is entered)
-      span_id = static_cast<unsigned>(t) / static_cast<unsigned>(A.span);
-      span_end = (span_id + 1) * A.span;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          gt[v][q] = has[v] ? __ldg(A.gate + span_id * (nv * 8LL) + (lane + v * G) * 8 + q) : 0.f;
-    }
-    // p = alpha dout (or dxn); n = xh g; s = sum p n (times the gate)
-    float s = 0.f;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  auto issue = [&](int t, int stage) {   // always one group of copies, of nothing past the rows
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float fu[8], fx[8];
-      unpack8(cu[v], fu);
-      unpack8(cx[v], fx);
+      const bool live = t < row1 && has[v];
+      const long long at = live ? static_cast<long long>(t) * nv + lane + v * G : 0;
+      copy16(base + 16 * slot(stage, 0, v), A.up + at, live);
+      copy16(base + 16 * slot(stage, 1, v), A.x + at, live);
+      if (RES) copy16(base + 16 * slot(stage, 2, v), A.dres + at, live);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto row_scalars = [&](int t, float& r, float& sg) {
+    r = 1.f;
+    sg = kVec ? 1.f : A.scale;
+    if (t < row1) {
+      if (NORM) r = __ldg(A.rstd + t);
+      if (GATE == kGateScalar) sg *= __ldg(A.gate + (A.span == 1 ? t : t / A.span));
+    }
+  };
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float p = A.scale * fu[q];
-        const float xh = NORM ? fx[q] * rs : fx[q];
-        const float pn = p * xh;
-        if (NORM) dg[v][q] = fmaf(pn, GATE == kGateVector ? gt[v][q] : gs, dg[v][q]);
-        const float pg = pn * g[v][q];
-        if (GATE == kGateVector) {
-          dgt[v][q] += pg;
-          s = fmaf(pg, gt[v][q], s);
-        } else {
-          s += pg;
-        }
+  for (int st = 0; st + 1 < kStages; ++st) issue(row0 + st, st);
+  float rs, sg;
+  row_scalars(row0, rs, sg);
+  int span_id = 0;
+  long long span_end = -1;
+  for (int i = 0; i < A.chunk; ++i) {   // every group of a block runs every step
+    const int t = row0 + i;
+    const bool live = t < row1;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    issue(t + kStages - 1, (i + kStages - 1) % kStages);   // the slots of row t - 1, read by now
+    const int stage = i % kStages;
+    if (kVec && live && t >= span_end) {   // a span begins (or is entered)
+      span_id = t / A.span;
+      span_end = (span_id + 1LL) * A.span;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (!has[v]) break;
+        const int c = (lane + v * G) * 8;
+        float gn[8];
+        load8f(A.gate + span_id * (nv * 8LL) + c, k[v]);
+        if (NORM) load8f(A.gain + c, gn);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) k[v][q] *= NORM ? A.scale * gn[q] : A.scale;
       }
     }
-    if (NORM || GATE == kGateScalar) s = group_sum(s, G, red, static_cast<int>(i));
-    if (GATE == kGateScalar) {
-      if (live && lane == 0) A.row_dot[t] = s;
-      s *= gs;
+    float nrs, nsg;
+    row_scalars(t + 1, nrs, nsg);
+    float a[V][8], b[V][8];
+    float s = 0.f;
+    const float w = rs * (kVec ? 1.f : sg);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      unpack8(ring[slot(stage, 0, v)], a[v]);
+      unpack8(ring[slot(stage, 1, v)], b[v]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float p = a[v][q] * b[v][q];
+        if (kVec) e[v][q] = fmaf(p, rs, e[v][q]);
+        else if (NORM) dg[v][q] = fmaf(p, w, dg[v][q]);
+        s = fmaf(p, k[v][q], s);
+      }
     }
-    const float mean = s * A.inv_d;
+    if (NORM || GATE == kGateScalar) s = group.sum(s, G, i);
+    if (GATE == kGateScalar && live && lane == 0) A.row_dot[t] = A.scale * rs * s;
+    const float wa = rs * sg, wb = -(rs * rs) * (s * rs * sg * A.inv_d);
     if (live) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (!has[v]) continue;
-        float fu[8], fx[8], fr[8];
-        unpack8(cu[v], fu);
-        unpack8(cx[v], fx);
-        unpack8(cr[v], fr);
+        if (!has[v]) break;
+        float o[8];
+        if (RES) unpack8(ring[slot(stage, 2, v)], o);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float dn = A.scale * fu[q] * (GATE == kGateVector ? gt[v][q] : gs);
-          if (NORM) {
-            const float xh = fx[q] * rs;
-            fr[q] = fmaf(rs, fmaf(-xh, mean, g[v][q] * dn), fr[q]);
-          } else {
-            fr[q] += dn;
-          }
+          float d = RES ? o[q] : 0.f;
+          if (NORM) d = RES ? fmaf(wb, b[v][q], d) : wb * b[v][q];
+          o[q] = fmaf(wa, k[v][q] * a[v][q], d);
         }
-        stg_v4(A.dx + t * nv + lane + v * G, pack8(fr));
+        stg_v4(A.dx + static_cast<long long>(t) * nv + lane + v * G, pack8(o));
       }
     }
-    if (GATE == kGateVector && live && (t + 1 == span_end || t + 1 == row1)) {
-      const long long begin = span_id * A.span;
-      const long long end = span_end < A.T ? span_end : A.T;
+    if (kVec && live && (t + 1 == span_end || t + 1 == row1)) {
+      const long long begin = static_cast<long long>(span_id) * A.span;
+      const long long end = min(span_end, static_cast<long long>(A.T));
       float* to = begin < row0 ? A.part_gate0 + worker * (nv * 8LL)
                   : end > row1 ? A.part_gate1 + worker * (nv * 8LL)
                                : A.dgate + span_id * (nv * 8LL);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (has[v]) store_cols(to + (lane + v * G) * 8, dgt[v]);
+        if (!has[v]) break;
+        const int c = (lane + v * G) * 8;
+        float gn[8], gt[8], o[8];
+        if (NORM) {
+          load8f(A.gain + c, gn);
+          load8f(A.gate + span_id * (nv * 8LL) + c, gt);
+        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) dgt[v][q] = 0.f;
+        for (int q = 0; q < 8; ++q) {
+          const float se = A.scale * e[v][q];
+          o[q] = NORM ? gn[q] * se : se;
+          if (NORM) dg[v][q] = fmaf(gt[q], se, dg[v][q]);
+          e[v][q] = 0.f;
+        }
+        store_cols(to + c, o);
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      cu[v] = nu[v];
-      cx[v] = nx[v];
-      cr[v] = nr[v];
-    }
     rs = nrs;
-    gs = ngs;
+    sg = nsg;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (NORM && row0 < A.T) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -389,46 +671,45 @@ __global__ void __launch_bounds__(1024, 1) norm_backward_kernel(BackwardArgs A) 
   }
 }
 
-// Joins the groups' column sums: blockIdx.x picks 32 columns, 8 warps take the
-// groups in turn, then one fixed tree. blockIdx.y = 0 sums dgain; y = 1 + w the
-// span that begins in group w's rows and ends in a later group's.
+// Joins the groups' column sums: blockIdx.x picks 32 columns, the warps take the
+// groups in turn, then one fixed tree. blockIdx.y = 0 sums dgain; the others
+// stand for the spans (by_span) or for the groups, whichever are fewer, and sum
+// the span if it crosses groups (of a group: the span that begins in its rows and
+// goes on past them).
 constexpr int kJoinWarps = 16;
 
 __global__ void __launch_bounds__(kJoinWarps * 32)
 norm_join_kernel(const float* part_gain, const float* part_gate0, const float* part_gate1, int d,
-                 long long workers, long long chunk, long long T, long long span, float* dgain,
+                 int workers, int chunk, int T, int span, int by_span, float* dgain,
                  float* dgate) {
   pdl_enter();
   __shared__ float acc[kJoinWarps][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   const float* first = nullptr;   // a row added to the sum of rows [a, b) of `rest`
-  const float* rest;
-  float* to;
-  long long a, b;
+  const float* rest = part_gain;
+  float* to = dgain;
+  int a = 0, b = workers;
   if (blockIdx.y == 0) {
     if (!dgain) return;
-    rest = part_gain;
-    a = 0;
-    b = workers;
-    to = dgain;
   } else {
-    const long long w = blockIdx.y - 1;
-    const long long row0 = w * chunk, row1 = row0 + chunk;
-    if (row1 >= T) return;                                     // nothing goes on past the last row
-    const long long s = (row1 - 1) / span;
-    const long long begin = s * span, end = (s + 1) * span < T ? (s + 1) * span : T;
-    if (begin < row0 || end <= row1) return;
-    first = part_gate1 + w * d;
+    const long long k = blockIdx.y - 1;
+    const long long s = by_span ? k : min((k + 1) * chunk, static_cast<long long>(T)) - 1;
+    const long long id = by_span ? s : s / span;
+    const long long begin = id * span, end = min(begin + span, static_cast<long long>(T));
+    const int w = static_cast<int>(by_span ? begin / chunk : k);
+    const long long row1 = (w + 1LL) * chunk;
+    if (begin < static_cast<long long>(w) * chunk || end <= row1) return;
+    first = part_gate1 + static_cast<long long>(w) * d;
     rest = part_gate0;
     a = w + 1;
-    b = (end - 1) / chunk + 1;
-    to = dgate + s * d;
+    b = static_cast<int>((end - 1) / chunk) + 1;
+    to = dgate + id * d;
   }
   float s = 0.f;
   if (c < d) {
-#pragma unroll 4
-    for (long long w = a + warp; w < b; w += kJoinWarps) s += __ldcg(rest + w * d + c);
+#pragma unroll 8
+    for (int w = a + warp; w < b; w += kJoinWarps) s += __ldcg(rest + static_cast<long long>(w) * d + c);
   }
   acc[warp][lane] = s;
   __syncthreads();
@@ -469,71 +750,79 @@ __global__ void zero_floats_kernel(float* a, long long na, float* b, long long n
 // Groups of the gradient kernels and the rows each takes.
 struct BackwardPlan {
   RowPlan rows;
-  int grid;
-  long long chunk, workers;
+  ChunkPlan chunks;
+  int V;
 };
 
 BackwardPlan plan_backward(int T, int d) {
   BackwardPlan p;
-  p.rows = plan_rows(d);
-  const long long most = static_cast<long long>(num_sms()) * resident(p.rows) * p.rows.groups;
-  p.chunk = (T + most - 1) / most;
-  if (p.chunk < 1) p.chunk = 1;
-  p.workers = (T + p.chunk - 1) / p.chunk;
-  p.grid = static_cast<int>((p.workers + p.rows.groups - 1) / p.rows.groups);
+  p.V = d <= 8 * NB_CUT ? 1 : d <= 8192 ? 2 : 4;
+  p.rows = plan_rows(d, p.V);
+  p.chunks = plan_chunks(T, p.rows, std::max(1, ring_threads(p.V) / p.rows.block()));
   return p;
 }
 
 bool norm_shape_ok(int T, int d) { return T >= 0 && d >= 8 && d % 8 == 0; }
 
+template <int V, bool RES, bool NORM, int GATE>
+int run_backward(const BackwardPlan& p, const BackwardArgs& a, cudaStream_t st) {
+  static thread_local int configured = -1;
+  const size_t smem = sizeof(uint4) * ring_stages(V) * (RES ? 3 : 2) * V * p.rows.block();
+  return launch_big(norm_backward_kernel<V, RES, NORM, GATE>, configured, p.chunks.grid,
+                    p.rows.block(), smem, st, a);
+}
+
 template <int V>
 int run_backward(const BackwardPlan& p, const BackwardArgs& a, bool norm, int gate,
                  cudaStream_t st) {
-  auto go = [&](auto kern) { return launch_pdl(kern, p.grid, p.rows.block(), 0, st, 1, a); };
+  if (a.dres) return run_backward<V, true, true, kGateNone>(p, a, st);
   if (norm) {
-    if (gate == kGateNone) return go(norm_backward_kernel<V, true, kGateNone>);
-    if (gate == kGateScalar) return go(norm_backward_kernel<V, true, kGateScalar>);
-    return go(norm_backward_kernel<V, true, kGateVector>);
+    if (gate == kGateNone) return run_backward<V, false, true, kGateNone>(p, a, st);
+    if (gate == kGateScalar) return run_backward<V, false, true, kGateScalar>(p, a, st);
+    return run_backward<V, false, true, kGateVector>(p, a, st);
   }
-  if (gate == kGateNone) return go(norm_backward_kernel<V, false, kGateNone>);
-  if (gate == kGateScalar) return go(norm_backward_kernel<V, false, kGateScalar>);
-  return go(norm_backward_kernel<V, false, kGateVector>);
+  if (gate == kGateNone) return run_backward<V, false, false, kGateNone>(p, a, st);
+  if (gate == kGateScalar) return run_backward<V, false, false, kGateScalar>(p, a, st);
+  return run_backward<V, false, false, kGateVector>(p, a, st);
 }
 
 int launch_backward(const char* name, BackwardArgs a, int T, int d, bool norm, int gate,
                     float* dgain, void* ws, cudaStream_t st) {
   const BackwardPlan p = plan_backward(T, d);
   float* scratch = reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspaceHeader);
+  const size_t slots = static_cast<size_t>(p.chunks.workers) * d;
   a.part_gain = scratch;
-  a.part_gate0 = a.part_gain + p.workers * d;
-  a.part_gate1 = a.part_gate0 + p.workers * d;
+  a.part_gate0 = scratch + slots;
+  a.part_gate1 = scratch + 2 * slots;
   const bool direct = gate == kGateScalar && a.span == 1;
-  a.row_dot = direct ? a.dgate : a.part_gate1 + p.workers * d;
+  a.row_dot = direct ? a.dgate : scratch + 3 * slots;
   a.T = T;
-  a.chunk = p.chunk;
+  a.chunk = p.chunks.chunk;
   a.inv_d = 1.f / static_cast<float>(d);
   a.nv = d / 8;
   a.G = p.rows.G;
   int rc;
   {
     ProfScope prof(name, st);
-    rc = p.rows.V == 1 ? run_backward<1>(p, a, norm, gate, st)
-                       : run_backward<2>(p, a, norm, gate, st);
+    rc = p.V == 1   ? run_backward<1>(p, a, norm, gate, st)
+         : p.V == 2 ? run_backward<2>(p, a, norm, gate, st)
+                    : run_backward<4>(p, a, norm, gate, st);
   }
   if (rc != MOE_OK) return rc;
   if (norm || gate == kGateVector) {
     ProfScope prof("norm_join", st);
-    const dim3 grid((d + 31) / 32, gate == kGateVector ? 1 + static_cast<unsigned>(p.workers) : 1);
+    const int spans = gate == kGateVector ? (T - 1) / a.span + 1 : 0;
+    const dim3 grid((d + 31) / 32, 1 + std::min(spans, p.chunks.workers));
     rc = launch_pdl(norm_join_kernel, grid, kJoinWarps * 32, 0, st, 1, a.part_gain, a.part_gate0,
-                    a.part_gate1, d, p.workers, p.chunk, static_cast<long long>(T), a.span,
-                    norm ? dgain : nullptr, a.dgate);
+                    a.part_gate1, d, p.chunks.workers, p.chunks.chunk, T, a.span,
+                    static_cast<int>(spans <= p.chunks.workers), norm ? dgain : nullptr, a.dgate);
     if (rc != MOE_OK) return rc;
   }
   if (gate == kGateScalar && !direct) {
     ProfScope prof("norm_join_rows", st);
-    const long long rows = (T + a.span - 1) / a.span;
+    const int rows = (T - 1) / a.span + 1;
     rc = launch_pdl(norm_join_rows_kernel, static_cast<unsigned>(rows), 256, 0, st, 1, a.row_dot,
-                    static_cast<long long>(T), a.span, a.dgate);
+                    static_cast<long long>(T), static_cast<long long>(a.span), a.dgate);
   }
   return rc;
 }
@@ -552,7 +841,7 @@ int zero_sums(float* dgain, long long n_gain, float* dgate, long long n_gate, cu
 size_t norm_backward_workspace(int T, int d) {
   if (!norm_shape_ok(T, d) || d > kMaxD) return 0;
   const BackwardPlan p = plan_backward(T, d);
-  return kWorkspaceHeader + sizeof(float) * (static_cast<size_t>(p.workers) * d * 3 + T);
+  return kWorkspaceHeader + sizeof(float) * (static_cast<size_t>(p.chunks.workers) * d * 3 + T);
 }
 
 }  // namespace moe
@@ -566,19 +855,31 @@ extern "C" int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, f
   if (!x || !gain || !xn || !rstd) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(gain) || !aligned16(xn) || !aligned16(rstd))
     return MOE_ERR_MISALIGNED;
-  const RowPlan p = plan_rows(d);
-  const long long blocks = (static_cast<long long>(T) + p.groups - 1) / p.groups;
-  const long long cap = static_cast<long long>(num_sms()) * resident(p);
-  const unsigned grid = static_cast<unsigned>(std::min(blocks, cap));
+  const int nv = d / 8;
+  const float inv_d = 1.f / static_cast<float>(d);
+  auto xi = reinterpret_cast<const uint4*>(x);
+  auto xo = reinterpret_cast<uint4*>(xn);
   cudaStream_t st = as_stream(stream);
   ProfScope prof("norm_in", st);
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, p.block(), 0, st, 1, reinterpret_cast<const uint4*>(x), gain, eps,
-                      1.f / static_cast<float>(d), static_cast<long long>(T), d / 8, p.G,
-                      reinterpret_cast<uint4*>(xn), rstd);
+  if (few_rows(T)) {
+    const int V = d <= 8192 ? 1 : 2;
+    auto go = [&](auto kern) {
+      return launch_pdl(kern, T, plan_rows(d, V).G, 0, st, 1, xi, gain, eps, inv_d, nv, xo, rstd);
+    };
+    return V == 1 ? go(norm_in_kernel<1>) : go(norm_in_kernel<2>);
+  }
+  auto go = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    static thread_local int configured = -1;
+    const RowPlan p = plan_rows(d, V);
+    const ChunkPlan c = plan_chunks(T, p, std::max(1, in_threads(V) / p.block()));
+    const size_t smem = sizeof(uint4) * in_stages(V) * V * p.block();
+    return launch_big(norm_in_ring_kernel<V>, configured, c.grid, p.block(), smem, st, xi, gain, eps,
+                      inv_d, T, c.chunk, nv, p.G, xo, rstd);
   };
-  if (p.V == 1) return go(norm_in_kernel<1>);
-  return go(norm_in_kernel<2>);
+  if (nv <= NI_CUT1) return go(std::integral_constant<int, 1>());
+  if (nv <= NI_CUT2) return go(std::integral_constant<int, 2>());
+  return go(std::integral_constant<int, 4>());
 }
 
 extern "C" int moe_norm_in_backward(const moe_bf16* dxn, const moe_bf16* x, const float* gain,
@@ -624,29 +925,47 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
   const void* ptrs[] = {y, topk_w, inv_perm, shared_y, resid, gain, gate, out, zsum, rstd};
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_MISALIGNED;
-  const RowPlan p = plan_rows(d);
-  const long long blocks = (static_cast<long long>(T) + p.groups - 1) / p.groups;
-  const long long cap = static_cast<long long>(num_sms()) * resident(p);
-  const unsigned grid = static_cast<unsigned>(std::min(blocks, cap));
   cudaStream_t st = as_stream(stream);
   ProfScope prof("norm_out", st);
+  const int nv = d / 8;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const unsigned gate_span = gate ? span : 1;
+  auto yi = reinterpret_cast<const uint4*>(y), si = reinterpret_cast<const uint4*>(shared_y);
+  auto ri = reinterpret_cast<const uint4*>(resid);
+  auto oo = reinterpret_cast<uint4*>(out), zo = reinterpret_cast<uint4*>(zsum);
+  const RowPlan wide = plan_rows(d, 1);
+  const int arrays = K + 1 + (shared_y ? 1 : 0);
+  const int S = arrays <= 4 ? 4 : 2;
+  const size_t smem = sizeof(uint4) * S * arrays * wide.block();
+  if (!few_rows(T) && nv <= 1024 && smem <= kSmemPerBlock - 1024) {
+    const int resident = std::min<int>(std::max(1, 1024 / wide.block()),
+                                       kSmemPerSm / static_cast<int>(smem + kSmemReserved));
+    const ChunkPlan c = plan_chunks(T, wide, std::max(1, resident));
+    static thread_local int configured[2] = {-1, -1};
+    auto go = [&](auto kern) {
+      return launch_big(kern, configured[S == 2], c.grid, wide.block(), smem, st, yi, topk_w,
+                        inv_perm, K, si, ri, gain, gate, gate_span, gate_cols, scale, eps, inv_d, T,
+                        c.chunk, nv, wide.G, oo, zo, rstd);
+    };
+    return S == 2 ? go(norm_out_ring_kernel<2>) : go(norm_out_ring_kernel<4>);
+  }
+  const int V = few_rows(T) && nv <= 1024 ? 1 : nv <= 1024 ? 4 : 8;
+  const RowPlan p = plan_rows(d, V);
+  const unsigned grid = (static_cast<unsigned>(T) + p.groups - 1) / p.groups;
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, p.block(), 0, st, 1, reinterpret_cast<const uint4*>(y), topk_w,
-                      inv_perm, K, reinterpret_cast<const uint4*>(shared_y),
-                      reinterpret_cast<const uint4*>(resid), gain, gate,
-                      static_cast<unsigned>(gate ? span : 1), gate_cols, scale, eps,
-                      1.f / static_cast<float>(d), static_cast<long long>(T), d / 8, p.G,
-                      reinterpret_cast<uint4*>(out), reinterpret_cast<uint4*>(zsum), rstd);
+    return launch_pdl(kern, grid, p.block(), 0, st, 1, yi, topk_w, inv_perm, K, si, ri, gain, gate,
+                      gate_span, gate_cols, scale, eps, inv_d, T, nv, p.G, oo, zo, rstd);
   };
   auto by_k = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (K == 1) return go(norm_out_kernel<1, V>);
-    if (K <= 2) return go(norm_out_kernel<2, V>);
-    if (K <= 4) return go(norm_out_kernel<4, V>);
-    return go(norm_out_kernel<8, V>);
+    constexpr int N = decltype(v)::value;
+    if (K == 1) return go(norm_out_kernel<1, N>);
+    if (K <= 2) return go(norm_out_kernel<2, N>);
+    if (K <= 4) return go(norm_out_kernel<4, N>);
+    return go(norm_out_kernel<8, N>);
   };
-  if (p.V == 1) return by_k(std::integral_constant<int, 1>());
-  return by_k(std::integral_constant<int, 2>());
+  if (V == 1) return by_k(std::integral_constant<int, 1>());
+  if (V == 4) return by_k(std::integral_constant<int, 4>());
+  return by_k(std::integral_constant<int, 8>());
 }
 
 extern "C" int moe_norm_out_backward(const moe_bf16* dout, const moe_bf16* zsum, const float* rstd,

@@ -28,9 +28,17 @@
 namespace moe {
 namespace {
 
+#ifndef W4_CUT1
+#define W4_CUT1 6
+#endif
+#ifndef W4_CUT2
+#define W4_CUT2 12
+#endif
+#ifndef W4_STAGES
+#define W4_STAGES 4
+#endif
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTokens = 32;       // rows of an expert per pass over its weights
 
 // ----------------------------------------------------------------- quantizer
 // s = max|w| / 7 rounded up to bf16, q = rint(w fl32(1 / s)) + 8 in 1 .. 15. One
@@ -132,84 +140,149 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t w, int n) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Half a tile (32 K): two products per 8 rows of X, added scaled into acc.
-template <int NT, bool FLUSH>
+// The same into a fresh sum.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Half a tile (32 K): two products per 8 rows of X. FIRST starts the group's
+// sums, LAST adds them scaled into acc.
+template <int NT, bool FIRST, bool LAST>
 __device__ __forceinline__ void half_tile(uint32_t w0, uint32_t w1, const uint4 (&x)[NT],
                                           float (&part)[NT][4], float s0, float s1,
                                           float (&acc)[NT][4]) {
+  const uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
+  const uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a0 = pair_of(w0, 2 * h), a1 = pair_of(w1, 2 * h);
-    const uint32_t a2 = pair_of(w0, 2 * h + 1), a3 = pair_of(w1, 2 * h + 1);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      mma16816(part[n], a0, a1, a2, a3, h ? x[n].z : x[n].x, h ? x[n].w : x[n].y);
-  }
-  if (FLUSH) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < NT; ++n) {
+    if (FIRST) mma16816_first(part[n], a0, x[n].x, x[n].y);
+    else mma16816(part[n], a0, x[n].x, x[n].y);
+    mma16816(part[n], a1, x[n].z, x[n].w);
+    if (LAST) {
       acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
       acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
       acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
       acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
     }
   }
 }
 
-// acc[n][.] += the tile's outputs over k-tiles [k0, k1) for the 8 NT rows of X
-// whose row pointers (at this lane's column offset) are xr[n]; null: a zero row.
-// wt: this lane's 16 bytes of k-tile 0; sc: this lane's scale pair of group 0.
+// Each warp streams its weights through a ring of its own in shared memory: a
+// stage is two k-tiles and their scales, every lane copies the 16 bytes per tile
+// that it will read itself, a few lanes also the scales. cp.async and not
+// registers: 3 KB a warp stay in flight and the accumulators keep the registers.
+constexpr int kStages = W4_STAGES;
+constexpr int scale_vecs(int group) { return 256 / group; }           // 16-byte pieces a stage
+constexpr int stage_vecs(int group) { return 64 + scale_vecs(group); }
+constexpr size_t ring_bytes(int group) {
+  return sizeof(uint4) * kWarps * kStages * stage_vecs(group);
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Half h (32 K) of the p-th k-tile of the lane's rows of X.
 template <int NT>
-__device__ __forceinline__ void product(const uint4* wt, const uint32_t* sc, int group, int k0,
-                                        int k1, const uint8_t* const (&xr)[NT],
-                                        float (&acc)[NT][4]) {
-  constexpr int kDepth = 4;   // weight tiles in flight
-  uint4 w[kDepth];
+__device__ __forceinline__ void load_x(const uint4* const (&xr)[NT], int p, int h, uint4 (&x)[NT]) {
 #pragma unroll
-  for (int p = 0; p < kDepth; ++p)
-    if (k0 + p < k1) w[p] = ldg_nc_v4(wt + static_cast<long long>(k0 + p) * 32);
-  float part[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int kb = k0; kb < k1; kb += kDepth) {
-#pragma unroll
-    for (int p = 0; p < kDepth; ++p) {
-      const int k = kb + p;
-      if (k < k1) {
-        uint4 x0[NT], x1[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4* r = reinterpret_cast<const uint4*>(xr[n] + k * 128LL);
-          x0[n] = xr[n] ? __ldg(r) : zero;
-          x1[n] = xr[n] ? __ldg(r + 4) : zero;
-        }
-        const uint4 cur = w[p];
-        if (k + kDepth < k1) w[p] = ldg_nc_v4(wt + static_cast<long long>(k + kDepth) * 32);
-        if (group == 32) {
-          const uint32_t sa = __ldg(sc + 16LL * k), sb = __ldg(sc + 16LL * k + 8);
-          half_tile<NT, true>(cur.x, cur.y, x0, part, bf16_lo(sa), bf16_hi(sa), acc);
-          half_tile<NT, true>(cur.z, cur.w, x1, part, bf16_lo(sb), bf16_hi(sb), acc);
-        } else {
-          const uint32_t s = __ldg(sc + (group == 64 ? 8LL * k : 8LL * (k >> 1)));
-          half_tile<NT, false>(cur.x, cur.y, x0, part, 0.f, 0.f, acc);
-          half_tile<NT, true>(cur.z, cur.w, x1, part, bf16_lo(s), bf16_hi(s), acc);
-        }
-      }
+  for (int n = 0; n < NT; ++n) x[n] = __ldg(xr[n] + 8 * p + 4 * h);
+}
+
+// A warp's weights: `count` k-tiles of one tile of outputs.
+template <int GROUP>
+struct Stream {
+  const uint4* codes;    // this lane's 16 bytes of the next stage to copy
+  const uint4* scales;
+  uint4* ring;
+  uint32_t ring_addr;
+  int left;              // k-tiles not yet copied
+  int slot;              // stage slot of the next copy
+
+  __device__ __forceinline__ void issue() {
+    const int lane = threadIdx.x & 31;
+    if (left > 0) {
+      const uint32_t to = ring_addr + slot * (16 * stage_vecs(GROUP));
+      copy16(to + 16 * lane, codes);
+      if (left > 1) copy16(to + 512 + 16 * lane, codes + 32);
+      // a last stage of one tile has half the scales (groups of 128 never end so)
+      if (lane < scale_vecs(GROUP) && (left > 1 || lane < (scale_vecs(GROUP) + 1) / 2))
+        copy16(to + 1024 + 16 * lane, scales + lane);
+      codes += 64;
+      scales += scale_vecs(GROUP);
+      left -= 2;
+      slot = slot + 1 == kStages ? 0 : slot + 1;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
+// acc[n][.] += the tile's outputs over the stream's k-tiles, for the 8 NT rows of
+// X at xr[n] (this lane's share of the first k-tile). With 8 rows X is loaded a
+// stage ahead; with more, the registers for that are missing.
+template <int NT, int GROUP>
+__device__ __forceinline__ void product(Stream<GROUP>& st, int count, const uint4* (&xr)[NT],
+                                        float (&acc)[NT][4]) {
+  constexpr bool kAhead = NT == 1;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  uint4 nx[2][2][NT];
+  if (kAhead) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      if (p < count) {
+        load_x<NT>(xr, p, 0, nx[p][0]);
+        load_x<NT>(xr, p, 1, nx[p][1]);
+      }
+  }
+  int slot = 0;
+  for (int k = 0; k < count; k += 2) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();   // the scales of this stage are there; all lanes are done with the last one
+    st.issue();
+    const uint4* stage = st.ring + slot * stage_vecs(GROUP);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(stage + 64) + g;
+    uint4 x[2][2][NT];
+    if (kAhead) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[p][h][n] = nx[p][h][n];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (k + 2 + p < count) {
+          load_x<NT>(xr, 2 + p, 0, nx[p][0]);
+          load_x<NT>(xr, 2 + p, 1, nx[p][1]);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (k + p >= count) break;
+      const uint4 w = stage[32 * p + lane];
+      const uint32_t s0 = sc[GROUP == 32 ? 16 * p : GROUP == 64 ? 8 * p : 0];
+      const uint32_t s1 = GROUP == 32 ? sc[16 * p + 8] : s0;
+      float part[NT][4];
+      if (!kAhead) load_x<NT>(xr, p, 0, x[p][0]);
+      half_tile<NT, true, GROUP == 32>(w.x, w.y, x[p][0], part, bf16_lo(s0), bf16_hi(s0), acc);
+      if (!kAhead) load_x<NT>(xr, p, 1, x[p][1]);
+      half_tile<NT, GROUP == 32, true>(w.z, w.w, x[p][1], part, bf16_lo(s1), bf16_hi(s1), acc);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xr[n] += 16;
   }
 }
 
@@ -219,13 +292,20 @@ __device__ __forceinline__ int expert_of(const int32_t* offsets, int E, int slot
   if (direct) return slot;
   const int lane = threadIdx.x & 31;
   int before = 0;
-  for (int base = 0; base < E; base += 32) {
-    const int e = base + lane;
-    const bool any = e < E && __ldg(offsets + e + 1) > __ldg(offsets + e);
-    const unsigned m = __ballot_sync(0xffffffffu, any);
-    const int n = __popc(m);
-    if (before + n > slot) return base + __fns(m, 0, slot - before + 1);
-    before += n;
+  for (int base = 0; base < E; base += 128) {   // 128 experts' offsets in one round trip
+    bool any[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = base + 32 * i + lane;
+      any[i] = e < E && __ldg(offsets + e + 1) > __ldg(offsets + e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned m = __ballot_sync(0xffffffffu, any[i]);
+      const int n = __popc(m);
+      if (before + n > slot) return base + 32 * i + static_cast<int>(__fns(m, 0, slot - before + 1));
+      before += n;
+    }
   }
   return -1;
 }
@@ -236,7 +316,7 @@ struct W4Args {
   int top_k;
   const int32_t* offsets;
   const uint4* tiles;
-  const uint32_t* scales;
+  const uint4* scales;
   __nv_bfloat16* out;       // h [M, I] or y [M, d]
   int E, M, K, N, nt, group;   // nt: tiles of outputs per expert; N: columns of out
   int x_rows;
@@ -244,9 +324,9 @@ struct W4Args {
 
 // One pass over a tile's weights for rows [r0, r0 + 8 NT) of the expert's rows
 // ending at r1, its K split over S warps of the block.
-template <bool GATE_UP, int S, int NT>
+template <bool GATE_UP, int S, int NT, int GROUP>
 __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int r0, int r1,
-                                     float (*red)[16 * 32]) {
+                                     uint4* ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int kt = A.K / 64;
@@ -256,29 +336,40 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[n][q] = 0.f;
+  if (S > 1) __syncthreads();   // the last pass has read the sums that lie over the rings
   if (live) {
-    const uint8_t* xr[NT];
+    const long long tile = static_cast<long long>(e) * A.nt + it;
+    // whole pairs of k-tiles to each split, so that groups of 128 stay in one
+    const int k0 = kt * ks / S & ~1, k1 = ks + 1 == S ? kt : kt * (ks + 1) / S & ~1;
+    Stream<GROUP> stream;
+    stream.codes = A.tiles + (tile * kt + k0) * 32 + lane;
+    stream.scales = A.scales + (tile * (A.K / GROUP) + k0 * 64 / GROUP) * 2;
+    stream.ring = ring + warp * kStages * stage_vecs(GROUP);
+    stream.ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(stream.ring));
+    stream.left = k1 - k0;
+    stream.slot = 0;
+    __syncwarp();   // every lane is done with the ring's last use
+    for (int p = 0; p + 1 < kStages; ++p) stream.issue();   // before the rows of X are looked up
+    const uint4* xr[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int p = r0 + 8 * n + g;
-      xr[n] = nullptr;
-      if (p < r1) {
-        long long row = p;
-        if (GATE_UP && A.perm) row = __ldg(A.perm + p) / A.top_k;
-        if (index_ok(row >= 0 && row < A.x_rows)) xr[n] = A.x + (row * A.K + 8 * c) * 2;
-      }
+      // past the expert's last row: that row again (the products' columns are
+      // apart, and these are not stored)
+      int row = min(r0 + 8 * n + g, r1 - 1);
+      if (GATE_UP && A.perm) row = __ldg(A.perm + row) / A.top_k;
+      if (!index_ok(row >= 0 && row < A.x_rows)) row = 0;
+      xr[n] = reinterpret_cast<const uint4*>(A.x) + static_cast<long long>(row) * (A.K / 8) + k0 * 8 + c;
     }
-    const long long tile = static_cast<long long>(e) * A.nt + it;
-    const int k0 = kt * ks / S, k1 = kt * (ks + 1) / S;
-    product<NT>(A.tiles + tile * kt * 32 + lane, A.scales + tile * (A.K / A.group) * 8 + g, A.group,
-                k0, k1, xr, acc);
+    product<NT, GROUP>(stream, k1 - k0, xr, acc);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (S > 1) {
-    __syncthreads();   // the last pass has read red
+    __syncthreads();   // every warp is done with its ring
+    float* red = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) red[warp][(n * 4 + q) * 32 + lane] = acc[n][q];
+      for (int q = 0; q < 4; ++q) red[(warp * 4 * NT + n * 4 + q) * 32 + lane] = acc[n][q];
     __syncthreads();
     if (ks != 0) return;
 #pragma unroll
@@ -286,7 +377,7 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int o = 1; o < S; ++o) acc[n][q] += red[warp + o][(n * 4 + q) * 32 + lane];
+        for (int o = 1; o < S; ++o) acc[n][q] += red[((warp + o) * 4 * NT + n * 4 + q) * 32 + lane];
   }
   if (!live) return;
 #pragma unroll
@@ -307,39 +398,61 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
   }
 }
 
-template <bool GATE_UP, int S>
-__global__ void __launch_bounds__(kThreads) w4_kernel(W4Args A) {
+// NTMAX: the most groups of 8 rows a pass takes (a power of two).
+template <bool GATE_UP, int S, int NTMAX, int GROUP>
+__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 3 : 2) w4_kernel(W4Args A) {
   pdl_enter();
-  __shared__ float red[S > 1 ? kWarps : 1][16 * 32];
+  extern __shared__ uint4 ring[];   // [warp][stage][codes, scales]
   const int e = expert_of(A.offsets, A.E, blockIdx.y, gridDim.y == static_cast<unsigned>(A.E));
   if (e < 0) return;
   int r0 = __ldg(A.offsets + e);
   const int r1 = min(__ldg(A.offsets + e + 1), A.M);
   const int warp = threadIdx.x >> 5;
   const int it = blockIdx.x * (kWarps / S) + warp / S, ks = warp % S;
-  for (; r0 < r1; r0 += kMaxTokens) {
+  for (; r0 < r1; r0 += 8 * NTMAX) {
     const int n = r1 - r0;
-    if (n <= 8) pass<GATE_UP, S, 1>(A, e, it, ks, r0, r1, red);
-    else if (n <= 16) pass<GATE_UP, S, 2>(A, e, it, ks, r0, r1, red);
-    else pass<GATE_UP, S, 4>(A, e, it, ks, r0, r1, red);
+    if (NTMAX == 1 || n <= 8) pass<GATE_UP, S, 1, GROUP>(A, e, it, ks, r0, r1, ring);
+    else if (NTMAX == 2 || n <= 16) pass<GATE_UP, S, 2, GROUP>(A, e, it, ks, r0, r1, ring);
+    else pass<GATE_UP, S, 4, GROUP>(A, e, it, ks, r0, r1, ring);
   }
 }
 
+template <bool GATE_UP, int NTMAX, int GROUP>
+int launch_split(int S, dim3 grid, const W4Args& a, cudaStream_t st) {
+  auto go = [&](auto kern) {
+#if W4_STAGES > 4
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+#endif
+    return launch_pdl(kern, grid, kThreads, ring_bytes(GROUP), st, 1, a);
+  };
+  static_assert(ring_bytes(GROUP) >= sizeof(float) * kWarps * NTMAX * 4 * 32, "sums over the rings");
+  if (S == 1) return go(w4_kernel<GATE_UP, 1, NTMAX, GROUP>);
+  if (S == 2) return go(w4_kernel<GATE_UP, 2, NTMAX, GROUP>);
+  if (S == 4) return go(w4_kernel<GATE_UP, 4, NTMAX, GROUP>);
+  return go(w4_kernel<GATE_UP, 8, NTMAX, GROUP>);
+}
+
+// most_rows: a bound on the rows of one expert.
 template <bool GATE_UP>
-int launch_w4(const char* name, const W4Args& a, cudaStream_t st) {
+int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st) {
   const int slots = std::min(a.E, a.M);
-  // Split K until the launch has about 16 warps per SM, a warp keeping four tiles at least.
-  const long long want = static_cast<long long>(num_sms()) * 16;
+  // Split K until the launch has about 24 warps per SM, a warp keeping four tiles at least.
+  const long long want = static_cast<long long>(num_sms()) * 24;
   const long long tiles = static_cast<long long>(slots) * a.nt;
   int S = 1;
   while (S < 8 && tiles * S < want && a.K / 64 >= 8 * S) S *= 2;
   ProfScope prof(name, st);
   const dim3 grid((a.nt + kWarps / S - 1) / (kWarps / S), slots);
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, kThreads, 0, st, 1, a); };
-  if (S == 1) return go(w4_kernel<GATE_UP, 1>);
-  if (S == 2) return go(w4_kernel<GATE_UP, 2>);
-  if (S == 4) return go(w4_kernel<GATE_UP, 4>);
-  return go(w4_kernel<GATE_UP, 8>);
+  auto by_group = [&](auto nt) {
+    constexpr int N = decltype(nt)::value;
+    if (a.group == 32) return launch_split<GATE_UP, N, 32>(S, grid, a, st);
+    if (a.group == 64) return launch_split<GATE_UP, N, 64>(S, grid, a, st);
+    return launch_split<GATE_UP, N, 128>(S, grid, a, st);
+  };
+  const int mean = std::min<long long>(most_rows, (a.M + a.E - 1) / a.E);
+  if (mean <= W4_CUT1) return by_group(std::integral_constant<int, 1>());
+  if (mean <= W4_CUT2) return by_group(std::integral_constant<int, 2>());
+  return by_group(std::integral_constant<int, 4>());
 }
 
 bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
@@ -419,7 +532,7 @@ extern "C" int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T,
   a.top_k = K;
   a.offsets = offsets;
   a.tiles = reinterpret_cast<const uint4*>(wgu);
-  a.scales = reinterpret_cast<const uint32_t*>(wgu_s);
+  a.scales = reinterpret_cast<const uint4*>(wgu_s);
   a.out = reinterpret_cast<__nv_bfloat16*>(h);
   a.E = E;
   a.M = M;
@@ -428,19 +541,19 @@ extern "C" int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T,
   a.nt = I / 8;
   a.group = group_gu;
   a.x_rows = T;
-  const int rc = launch_w4<true>("w4_gate_up", a, st);
+  const int rc = launch_w4<true>("w4_gate_up", a, perm ? T : M, st);
   if (rc != MOE_OK) return rc;
   a.x = reinterpret_cast<const uint8_t*>(h);
   a.perm = nullptr;
   a.tiles = reinterpret_cast<const uint4*>(wd);
-  a.scales = reinterpret_cast<const uint32_t*>(wd_s);
+  a.scales = reinterpret_cast<const uint4*>(wd_s);
   a.out = reinterpret_cast<__nv_bfloat16*>(y);
   a.K = I;
   a.N = d;
   a.nt = d / 16;
   a.group = group_d;
   a.x_rows = M;
-  return launch_w4<false>("w4_down", a, st);
+  return launch_w4<false>("w4_down", a, perm ? T : M, st);
 }
 
 namespace moe {
