@@ -958,8 +958,8 @@ def moe_w4_quantize_weights(w: torch.Tensor, group: int = 128, out=None):
 def moe_w4_pack_weights(codes_a: torch.Tensor, scales_a: torch.Tensor,
                         codes_b: Optional[torch.Tensor] = None,
                         scales_b: Optional[torch.Tensor] = None, out=None):
-    """Plain 4-bit weights laid out for moe_grouped_ffn_w4: (tiles uint8 [E, tiles, K/64, 512],
-    scales bf16 [E, tiles, K/group, 16]); gate (a) and up (b) share tiles."""
+    """Plain 4-bit weights laid out for moe_grouped_ffn_w4: (tiles uint8 [E, tiles, K/64, 1024],
+    scales bf16 [E, tiles, K/group, 32]); gate (a) and up (b) share tiles."""
     _need(codes_a, torch.uint8, 3, "codes_a")
     _need(scales_a, torch.bfloat16, 3, "scales_a")
     E, N, K = codes_a.shape[0], codes_a.shape[1], 2 * codes_a.shape[2]
@@ -974,15 +974,15 @@ def moe_w4_pack_weights(codes_a: torch.Tensor, scales_a: torch.Tensor,
         raise ValueError("codes_b and scales_b go together")
     _shaped(codes_b, torch.uint8, (E, N, K // 2), "codes_b", dev)
     _shaped(scales_b, torch.bfloat16, (E, N, ng), "scales_b", dev)
-    per = 16 if codes_b is None else 8
+    per = 32 if codes_b is None else 16
     if N % per:
         raise ValueError(f"N = {N} must be a multiple of {per}")
     if out is None:
-        out = (torch.empty(E, N // per, K // 64, 512, dtype=torch.uint8, device=dev),
-               torch.empty(E, N // per, ng, 16, dtype=torch.bfloat16, device=dev))
+        out = (torch.empty(E, N // per, K // 64, 1024, dtype=torch.uint8, device=dev),
+               torch.empty(E, N // per, ng, 32, dtype=torch.bfloat16, device=dev))
     else:
-        _shaped(out[0], torch.uint8, (E, N // per, K // 64, 512), "tiles", dev)
-        _shaped(out[1], torch.bfloat16, (E, N // per, ng, 16), "scales", dev)
+        _shaped(out[0], torch.uint8, (E, N // per, K // 64, 1024), "tiles", dev)
+        _shaped(out[1], torch.bfloat16, (E, N // per, ng, 32), "scales", dev)
     tiles, scales = out
     _check("moe_w4_pack_weights", load().moe_w4_pack_weights(
         _ptr(codes_a), _ptr(scales_a), _ptr(codes_b), _ptr(scales_b), E, N, K, group, _ptr(tiles),
@@ -996,10 +996,10 @@ def _w4_weight(w, E: int, per: int, name: str, dev):
     _need(tiles, torch.uint8, 4, name + " tiles")
     nt, kt = tiles.shape[1], tiles.shape[2]
     ng = scales.shape[2] if scales.dim() == 4 else 0
-    if tiles.shape[0] != E or tiles.shape[3] != 512 or ng < 1 or (64 * kt) % ng:
+    if tiles.shape[0] != E or tiles.shape[3] != 1024 or ng < 1 or (64 * kt) % ng:
         raise ValueError(f"{name} must come from moe_w4_pack_weights for {E} experts")
     _shaped(tiles, torch.uint8, tuple(tiles.shape), name + " tiles", dev)
-    _shaped(scales, torch.bfloat16, (E, nt, ng, 16), name + " scales", dev)
+    _shaped(scales, torch.bfloat16, (E, nt, ng, 32), name + " scales", dev)
     return nt * per, 64 * kt, 64 * kt // ng
 
 
@@ -1016,8 +1016,8 @@ def moe_grouped_ffn_w4(x: torch.Tensor, offsets: torch.Tensor, wgu, wd,
     E = offsets.numel() - 1
     M = T * int(K) if perm is not None else T
     _shaped(perm, torch.int32, (M,), "perm", dev)
-    I, k_gu, group_gu = _w4_weight(wgu, E, 8, "wgu", dev)
-    n_d, k_d, group_d = _w4_weight(wd, E, 16, "wd", dev)
+    I, k_gu, group_gu = _w4_weight(wgu, E, 16, "wgu", dev)
+    n_d, k_d, group_d = _w4_weight(wd, E, 32, "wd", dev)
     if k_gu != d or n_d != d or k_d != I or offsets.device != dev:
         raise ValueError(f"weights of [{k_gu} -> {I}] and [{k_d} -> {n_d}] do not fit x of {d}")
     ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_FFN_W4, T, E, K, 1, d, I) if ws is None else 0,

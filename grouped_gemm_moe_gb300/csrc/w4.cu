@@ -6,21 +6,21 @@
 //
 // With a few rows per expert the products are bound by reading the weights
 // (half a byte each, plus 2 / group), so the design is about a steady weight
-// stream. Weights are laid out once in the order the tensor cores take them:
-// tiles of 16 outputs x 64 K, 512 bytes, 16 bytes per lane, so one coalesced
-// load per warp and tile feeds four m16n8k16 products whose A is the weights
-// and whose 8 columns are rows of X. A code becomes the bf16 integer q - 8 in
-// registers (exact), so the products run on integers and the scale multiplies
-// the fp32 sums of a group: no weight is ever rounded. The lane's 16 elements
-// of K are two runs of 8, one in each half of the 64, which is the order the
-// rows of X are loaded in 16-byte pieces and keeps groups of 32 apart.
+// stream and few instructions per weight. Weights are laid out once in the order
+// the tensor cores take them: tiles of 32 outputs x 64 K, 1 KB, twice 16 bytes per
+// lane, which feed eight m16n8k16 products whose A is the weights and whose 8
+// columns are rows of X. A code becomes the bf16 integer 128 + q in registers
+// (exact, two instructions a pair), so the products run on integers and the
+// scale multiplies the fp32 sums of a group: no weight is ever rounded. The
+// lane's 16 elements of K are two runs of 8, one in each half of the 64, which is
+// the order the rows of X are loaded in 16-byte pieces and keeps groups of 32 apart.
 //
 // mma.sync and not tcgen05: the A operand is made in registers from 4-bit codes
 // and N is 8 to 32; tcgen05 would take it through shared memory or TMEM at
 // M = 128 for a product that is bound by HBM either way.
 //
-// Gate and up share tiles: outputs 0-7 of a tile are eight gate columns, 8-15 the
-// same up columns, which puts G and U of one element in one lane.
+// Gate and up share tiles: of each 16 outputs the first eight are gate columns,
+// the others the same up columns, which puts G and U of one element in one lane.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,14 +28,20 @@
 namespace moe {
 namespace {
 
+#ifndef W4_WANT
+#define W4_WANT 72
+#endif
+#ifndef W4_BLK
+#define W4_BLK 3
+#endif
+#ifndef W4_CUT0
+#define W4_CUT0 8
+#endif
 #ifndef W4_CUT1
 #define W4_CUT1 6
 #endif
 #ifndef W4_CUT2
 #define W4_CUT2 12
-#endif
-#ifndef W4_STAGES
-#define W4_STAGES 4
 #endif
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
@@ -76,15 +82,16 @@ w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K, int N, int group,
 }
 
 // ----------------------------------------------------------------- layout
-// The plain row of row `m` (0 .. 15) of tile `i`: outputs 16 i + m, or with gate
-// and up in one tile output 8 i + (m & 7) of gate (m < 8) or up.
+// The plain row of row m (0 .. 31) of tile i: output 32 i + m, or with gate and
+// up in one tile output 16 i + 8 (m / 16) + m % 8 of gate (m % 16 < 8) or up.
 __device__ __forceinline__ long long plain_row(long long e, int i, int m, int N, bool pair) {
-  return pair ? e * N + 8 * i + (m & 7) : e * N + 16 * i + m;
+  return e * N + (pair ? 16 * i + 8 * (m >> 4) + (m & 7) : 32 * i + m);
 }
 
-// One thread per word of a tile: word j of lane l is row l / 4 (j even) or that + 8
-// (odd), k = 32 (j / 2) + 8 (l % 4) + 0 .. 7; nibble n holds k offset 2 n
-// (n < 4) or 2 (n - 4) + 1, so word >> 4 n & 0x000f000f is the pair (2 n, 2 n + 1).
+// One thread per word of a tile: word j of lane l's piece h is row 16 h + l / 4
+// (j even) or that + 8 (odd), k = 32 (j / 2) + 8 (l % 4) + 0 .. 7; nibble n holds k
+// offset 2 n (n < 4) or 2 (n - 4) + 1, so word >> 4 n & 0x000f000f is the pair
+// (2 n, 2 n + 1).
 __global__ void __launch_bounds__(256)
 w4_pack_kernel(const uint8_t* __restrict__ ca, const uint8_t* __restrict__ cb, int N, int K, int nt,
                long long total, uint32_t* __restrict__ tiles) {
@@ -93,14 +100,15 @@ w4_pack_kernel(const uint8_t* __restrict__ ca, const uint8_t* __restrict__ cb, i
   if (i >= total) return;
   const int j = static_cast<int>(i & 3);
   const int l = static_cast<int>(i >> 2 & 31);
-  const long long tile = i >> 7;
+  const int h = static_cast<int>(i >> 7 & 1);
+  const long long tile = i >> 8;
   const int kt = K / 64;
   const int kb = static_cast<int>(tile % kt);
   const long long et = tile / kt;
   const int it = static_cast<int>(et % nt);
   const long long e = et / nt;
-  const int m = (l >> 2) + 8 * (j & 1);
-  const uint8_t* src = (cb && m >= 8) ? cb : ca;
+  const int m = 16 * h + (l >> 2) + 8 * (j & 1);
+  const uint8_t* src = (cb && (m & 8)) ? cb : ca;
   const long long k = 64LL * kb + 32 * (j >> 1) + 8 * (l & 3);
   const uint32_t w = *reinterpret_cast<const uint32_t*>(src + (plain_row(e, it, m, N, cb != nullptr) * K + k) / 2);
   uint32_t o = 0;
@@ -112,29 +120,37 @@ w4_pack_kernel(const uint8_t* __restrict__ ca, const uint8_t* __restrict__ cb, i
   tiles[i] = o;
 }
 
-// Scales [E][tile][K / group][16], rows m and m + 8 of a tile next to each other.
+// Scales [E][tile][K / group][8][4]: of row r's four, rows r, r + 8, r + 16, r + 24
+// of the tile, so that a lane takes its four with one load.
 __global__ void __launch_bounds__(256)
 w4_pack_scales_kernel(const uint16_t* __restrict__ sa, const uint16_t* __restrict__ sb, int N,
                       int ng, int nt, long long total, uint16_t* __restrict__ out) {
   pdl_enter();
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= total) return;
-  const int at = static_cast<int>(i & 15);
-  const int m = (at >> 1) + 8 * (at & 1);
-  const long long g = i >> 4;
+  const int m = static_cast<int>(i >> 2 & 7) + 8 * static_cast<int>(i & 3);
+  const long long g = i >> 5;
   const int gi = static_cast<int>(g % ng);
   const long long et = g / ng;
   const int it = static_cast<int>(et % nt);
   const long long e = et / nt;
-  const uint16_t* src = (sb && m >= 8) ? sb : sa;
+  const uint16_t* src = (sb && (m & 8)) ? sb : sa;
   out[i] = src[plain_row(e, it, m, N, sb != nullptr) * ng + gi];
 }
 
 // ----------------------------------------------------------------- products
-// The pair (2 n, 2 n + 1) of a word as bf16 integers q - 8: 0x4300 | q is
-// 128 + q, and subtracting 136 is exact.
+// The pair (2 n, 2 n + 1) of a word as bf16 integers 128 + q: 0x4300 | q, the
+// masking and the joining in one three-input logic instruction (two halve the
+// kernels' speed: the logic pipe is what they wait for first).
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, int n) {
-  uint32_t v = ((w >> (4 * n)) & 0x000f000fu) | 0x43004300u;
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"   // (a & b) | c
+      : "=r"(v) : "r"(w >> (4 * n)), "r"(0x000f000fu), "r"(0x43004300u));
+  return v;
+}
+
+// The same less 136, exactly q - 8.
+__device__ __forceinline__ uint32_t centred(uint32_t v) {
   const __nv_bfloat162 c = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), c);
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -157,35 +173,71 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Half a tile (32 K): two products per 8 rows of X. FIRST starts the group's
-// sums, LAST adds them scaled into acc.
-template <int NT, bool FIRST, bool LAST>
-__device__ __forceinline__ void half_tile(uint32_t w0, uint32_t w1, const uint4 (&x)[NT],
-                                          float (&part)[NT][4], float s0, float s1,
-                                          float (&acc)[NT][4]) {
-  const uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
-  const uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
+// A product into d from the sums c.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const float (&c)[4],
+                                              const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ void add_scaled(float (&acc)[4], float s0, float s1, const float (&p)[4]) {
+  acc[0] = fmaf(s0, p[0], acc[0]);
+  acc[1] = fmaf(s0, p[1], acc[1]);
+  acc[2] = fmaf(s1, p[2], acc[2]);
+  acc[3] = fmaf(s1, p[3], acc[3]);
+}
+
+// Half a tile (32 K) against 8 NT rows of X, scaled into acc[16 outputs][rows].
+// w: the lane's words of rows g and g + 8 in each 16 outputs; sc its four scales.
+// The codes come as 128 + q. With 8 rows two products by the constant -136
+// start the sums of both 16 outputs and take the excess out again (fp32 sums of
+// exact products, an error of about 2^-19 of the result), on tensor cores that
+// are mostly idle; with more rows those products would multiply, and the exact
+// subtractions that all rows share are the cheaper way.
+template <int NT>
+__device__ __forceinline__ void half_tile(uint32_t w00, uint32_t w01, uint32_t w10, uint32_t w11,
+                                          const uint4 (&x)[NT], uint2 sc, float (&acc)[2][NT][4]) {
+  const float s[2][2] = {{bf16_lo(sc.x), bf16_hi(sc.x)}, {bf16_lo(sc.y), bf16_hi(sc.y)}};
+  float less[4];
+  if (NT == 1) {
+    const uint32_t c[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
+    mma16816_first(less, c, x[0].x, x[0].y);
+    mma16816(less, c, x[0].z, x[0].w);
+  }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (FIRST) mma16816_first(part[n], a0, x[n].x, x[n].y);
-    else mma16816(part[n], a0, x[n].x, x[n].y);
-    mma16816(part[n], a1, x[n].z, x[n].w);
-    if (LAST) {
-      acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
-      acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
-      acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
-      acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t w0 = m ? w10 : w00, w1 = m ? w11 : w01;
+    uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
+    uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
+    if (NT > 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a0[i] = centred(a0[i]);
+        a1[i] = centred(a1[i]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float p[4];
+      if (NT == 1) mma16816_from(p, less, a0, x[n].x, x[n].y);
+      else mma16816_first(p, a0, x[n].x, x[n].y);
+      mma16816(p, a1, x[n].z, x[n].w);
+      add_scaled(acc[m][n], s[m][0], s[m][1], p);
     }
   }
 }
 
 // Each warp streams its weights through a ring of its own in shared memory: a
-// stage is two k-tiles and their scales, every lane copies the 16 bytes per tile
-// that it will read itself, a few lanes also the scales. cp.async and not
-// registers: 3 KB a warp stay in flight and the accumulators keep the registers.
-constexpr int kStages = W4_STAGES;
-constexpr int scale_vecs(int group) { return 256 / group; }           // 16-byte pieces a stage
-constexpr int stage_vecs(int group) { return 64 + scale_vecs(group); }
+// stage is two k-tiles and their scales, every lane copies the 16-byte pieces that
+// it will read itself, some lanes also the scales. cp.async and not registers:
+// 4.6 KB a warp stay in flight and the accumulators keep the registers.
+constexpr int kStages = 3;
+constexpr int kStageTiles = 2;
+constexpr int scale_vecs(int group) { return 256 * kStageTiles / group; }   // 16-byte pieces a stage
+constexpr int stage_vecs(int group) { return 64 * kStageTiles + scale_vecs(group); }
 constexpr size_t ring_bytes(int group) {
   return sizeof(uint4) * kWarps * kStages * stage_vecs(group);
 }
@@ -194,95 +246,103 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-// Half h (32 K) of the p-th k-tile of the lane's rows of X.
-template <int NT>
-__device__ __forceinline__ void load_x(const uint4* const (&xr)[NT], int p, int h, uint4 (&x)[NT]) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n) x[n] = __ldg(xr[n] + 8 * p + 4 * h);
-}
-
-// A warp's weights: `count` k-tiles of one tile of outputs.
+// A warp's weights: a run of k-tiles of one tile of outputs.
 template <int GROUP>
 struct Stream {
-  const uint4* codes;    // this lane's 16 bytes of the next stage to copy
-  const uint4* scales;
-  uint4* ring;
-  uint32_t ring_addr;
+  const uint4* codes;    // this lane's first piece of the next stage to copy
+  const uint4* scales;   // this lane's piece of its scales
+  const uint4* ring;
+  uint32_t to;           // this lane's place in the slot of the next copy
   int left;              // k-tiles not yet copied
-  int slot;              // stage slot of the next copy
+  int slot;
 
+  __device__ __forceinline__ void begin(const uint4* c, const uint4* s, uint4* r, int count) {
+    const int lane = threadIdx.x & 31;
+    codes = c + lane;
+    scales = s + lane;
+    ring = r;
+    to = static_cast<uint32_t>(__cvta_generic_to_shared(r)) + 16 * lane;
+    left = count;
+    slot = 0;
+  }
   __device__ __forceinline__ void issue() {
     const int lane = threadIdx.x & 31;
-    if (left > 0) {
-      const uint32_t to = ring_addr + slot * (16 * stage_vecs(GROUP));
-      copy16(to + 16 * lane, codes);
-      if (left > 1) copy16(to + 512 + 16 * lane, codes + 32);
-      // a last stage of one tile has half the scales (groups of 128 never end so)
-      if (lane < scale_vecs(GROUP) && (left > 1 || lane < (scale_vecs(GROUP) + 1) / 2))
-        copy16(to + 1024 + 16 * lane, scales + lane);
-      codes += 64;
-      scales += scale_vecs(GROUP);
-      left -= 2;
-      slot = slot + 1 == kStages ? 0 : slot + 1;
+    if (left >= kStageTiles) {
+#pragma unroll
+      for (int p = 0; p < 2 * kStageTiles; ++p) copy16(to + 512 * p, codes + 32 * p);
+      if (lane < scale_vecs(GROUP)) copy16(to + 1024 * kStageTiles, scales);
+    } else if (left > 0) {   // the rest: fewer tiles and their share of the scales
+      for (int p = 0; p < 2 * left; ++p) copy16(to + 512 * p, codes + 32 * p);
+      if (lane < scale_vecs(GROUP) * left / kStageTiles) copy16(to + 1024 * kStageTiles, scales);
     }
+    codes += 64 * kStageTiles;
+    scales += scale_vecs(GROUP);
+    left -= kStageTiles;
+    const bool wrap = ++slot == kStages;
+    to += 16 * stage_vecs(GROUP) - (wrap ? 16 * kStages * stage_vecs(GROUP) : 0);
+    slot = wrap ? 0 : slot;
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 };
 
-// acc[n][.] += the tile's outputs over the stream's k-tiles, for the 8 NT rows of
+// The lane's rows of X in the p-th k-tile: both halves of 32 K.
+template <int NT>
+__device__ __forceinline__ void load_x(const uint4* const (&xr)[NT], int p, uint4 (&x)[2][NT]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[h][n] = __ldg(xr[n] + 8 * p + 4 * h);
+}
+
+// One k-tile: w the lane's first piece of codes, sc its scales of the tile's first group.
+template <int NT, int GROUP>
+__device__ __forceinline__ void one_tile(const uint4* w, const uint2* sc, const uint4 (&x)[2][NT],
+                                         float (&acc)[2][NT][4]) {
+  const uint4 a = w[0], b = w[32];
+  const uint2 s0 = sc[0], s1 = GROUP == 32 ? sc[8] : s0;
+  half_tile<NT>(a.x, a.y, b.x, b.y, x[0], s0, acc);
+  half_tile<NT>(a.z, a.w, b.z, b.w, x[1], s1, acc);
+}
+
+constexpr int scale_step(int group) { return group == 32 ? 16 : group == 64 ? 8 : 0; }
+
+// acc += the tile's outputs over the stream's `count` k-tiles, for the 8 NT rows of
 // X at xr[n] (this lane's share of the first k-tile). With 8 rows X is loaded a
-// stage ahead; with more, the registers for that are missing.
+// tile ahead; with more, the registers for that are missing.
 template <int NT, int GROUP>
 __device__ __forceinline__ void product(Stream<GROUP>& st, int count, const uint4* (&xr)[NT],
-                                        float (&acc)[NT][4]) {
+                                        float (&acc)[2][NT][4]) {
+  static_assert(kStageTiles == 2, "X alternates between two buffers");
   constexpr bool kAhead = NT == 1;
   const int lane = threadIdx.x & 31, g = lane >> 2;
-  uint4 nx[2][2][NT];
-  if (kAhead) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      if (p < count) {
-        load_x<NT>(xr, p, 0, nx[p][0]);
-        load_x<NT>(xr, p, 1, nx[p][1]);
-      }
-  }
+  uint4 x[2][2][NT];   // by the parity of the tile
+  if (kAhead) load_x<NT>(xr, 0, x[0]);
   int slot = 0;
-  for (int k = 0; k < count; k += 2) {
+  for (; count > 0; count -= kStageTiles) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncwarp();   // the scales of this stage are there; all lanes are done with the last one
+    __syncwarp();   // this stage's scales are there, and all lanes are done with the last stage
     st.issue();
     const uint4* stage = st.ring + slot * stage_vecs(GROUP);
     slot = slot + 1 == kStages ? 0 : slot + 1;
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(stage + 64) + g;
-    uint4 x[2][2][NT];
-    if (kAhead) {
+    const uint2* sc = reinterpret_cast<const uint2*>(stage + 64 * kStageTiles) + g;
+    if (count > kStageTiles) {   // a whole stage, and more after it
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < kStageTiles; ++p) {
+        if (kAhead) load_x<NT>(xr, p + 1, x[(p + 1) & 1]);
+        else load_x<NT>(xr, p, x[p & 1]);
+        one_tile<NT, GROUP>(stage + 64 * p + lane, sc + scale_step(GROUP) * p, x[p & 1], acc);
+      }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < NT; ++n) xr[n] += 8 * kStageTiles;
+    } else {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) x[p][h][n] = nx[p][h][n];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (k + 2 + p < count) {
-          load_x<NT>(xr, 2 + p, 0, nx[p][0]);
-          load_x<NT>(xr, 2 + p, 1, nx[p][1]);
-        }
+      for (int p = 0; p < kStageTiles; ++p) {
+        if (p >= count) break;
+        if (!kAhead) load_x<NT>(xr, p, x[p & 1]);
+        else if (p + 1 < count) load_x<NT>(xr, p + 1, x[(p + 1) & 1]);
+        one_tile<NT, GROUP>(stage + 64 * p + lane, sc + scale_step(GROUP) * p, x[p & 1], acc);
+      }
     }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      if (k + p >= count) break;
-      const uint4 w = stage[32 * p + lane];
-      const uint32_t s0 = sc[GROUP == 32 ? 16 * p : GROUP == 64 ? 8 * p : 0];
-      const uint32_t s1 = GROUP == 32 ? sc[16 * p + 8] : s0;
-      float part[NT][4];
-      if (!kAhead) load_x<NT>(xr, p, 0, x[p][0]);
-      half_tile<NT, true, GROUP == 32>(w.x, w.y, x[p][0], part, bf16_lo(s0), bf16_hi(s0), acc);
-      if (!kAhead) load_x<NT>(xr, p, 1, x[p][1]);
-      half_tile<NT, GROUP == 32, true>(w.z, w.w, x[p][1], part, bf16_lo(s1), bf16_hi(s1), acc);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xr[n] += 16;
   }
 }
 
@@ -331,24 +391,22 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
   const int g = lane >> 2, c = lane & 3;
   const int kt = A.K / 64;
   const bool live = it < A.nt;
-  float acc[NT][4];
+  float acc[2][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[n][q] = 0.f;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
   if (S > 1) __syncthreads();   // the last pass has read the sums that lie over the rings
   if (live) {
     const long long tile = static_cast<long long>(e) * A.nt + it;
     // whole pairs of k-tiles to each split, so that groups of 128 stay in one
     const int k0 = kt * ks / S & ~1, k1 = ks + 1 == S ? kt : kt * (ks + 1) / S & ~1;
     Stream<GROUP> stream;
-    stream.codes = A.tiles + (tile * kt + k0) * 32 + lane;
-    stream.scales = A.scales + (tile * (A.K / GROUP) + k0 * 64 / GROUP) * 2;
-    stream.ring = ring + warp * kStages * stage_vecs(GROUP);
-    stream.ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(stream.ring));
-    stream.left = k1 - k0;
-    stream.slot = 0;
     __syncwarp();   // every lane is done with the ring's last use
+    stream.begin(A.tiles + (tile * kt + k0) * 64, A.scales + (tile * (A.K / GROUP) + k0 * 64 / GROUP) * 4,
+                 ring + warp * kStages * stage_vecs(GROUP), k1 - k0);
     for (int p = 0; p + 1 < kStages; ++p) stream.issue();   // before the rows of X are looked up
     const uint4* xr[NT];
 #pragma unroll
@@ -360,24 +418,22 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
       if (!index_ok(row >= 0 && row < A.x_rows)) row = 0;
       xr[n] = reinterpret_cast<const uint4*>(A.x) + static_cast<long long>(row) * (A.K / 8) + k0 * 8 + c;
     }
-    product<NT, GROUP>(stream, k1 - k0, xr, acc);
+    if (k0 < k1) product<NT, GROUP>(stream, k1 - k0, xr, acc);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (S > 1) {
+    constexpr int kSums = 8 * NT;   // per lane
     __syncthreads();   // every warp is done with its ring
     float* red = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) red[(warp * 4 * NT + n * 4 + q) * 32 + lane] = acc[n][q];
+    for (int i = 0; i < kSums; ++i) red[(warp * kSums + i) * 32 + lane] = acc[i / (4 * NT)][i / 4 % NT][i % 4];
     __syncthreads();
     if (ks != 0) return;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < kSums; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int o = 1; o < S; ++o) acc[n][q] += red[((warp + o) * 4 * NT + n * 4 + q) * 32 + lane];
+      for (int o = 1; o < S; ++o)
+        acc[i / (4 * NT)][i / 4 % NT][i % 4] += red[((warp + o) * kSums + i) * 32 + lane];
   }
   if (!live) return;
 #pragma unroll
@@ -387,12 +443,15 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
       const int p = r0 + 8 * n + 2 * c + q;
       if (p >= r1) continue;
       __nv_bfloat16* row = A.out + static_cast<long long>(p) * A.N;
-      if (GATE_UP) {
-        const float G = acc[n][q], U = acc[n][q + 2];
-        row[8 * it + g] = __float2bfloat16(__fdividef(G, 1.f + __expf(-G)) * U);
-      } else {
-        row[16 * it + g] = __float2bfloat16(acc[n][q]);
-        row[16 * it + g + 8] = __float2bfloat16(acc[n][q + 2]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (GATE_UP) {
+          const float G = acc[m][n][q], U = acc[m][n][q + 2];
+          row[16 * it + 8 * m + g] = __float2bfloat16(__fdividef(G, 1.f + __expf(-G)) * U);
+        } else {
+          row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][n][q]);
+          row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][n][q + 2]);
+        }
       }
     }
   }
@@ -400,7 +459,7 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
 
 // NTMAX: the most groups of 8 rows a pass takes (a power of two).
 template <bool GATE_UP, int S, int NTMAX, int GROUP>
-__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 3 : 2) w4_kernel(W4Args A) {
+__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? W4_BLK : 2) w4_kernel(W4Args A) {
   pdl_enter();
   extern __shared__ uint4 ring[];   // [warp][stage][codes, scales]
   const int e = expert_of(A.offsets, A.E, blockIdx.y, gridDim.y == static_cast<unsigned>(A.E));
@@ -417,27 +476,290 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 3 : 2) w4_kernel(W4Args
   }
 }
 
+// ----------------------------------------------------------------- few rows per expert
+// The same products for experts of about 8 rows or fewer, as one persistent block
+// of 16 warps per SM. An entry is up to 8 rows of one expert, an item one tile of
+// 32 outputs for one entry; a block takes a contiguous run of items, the same
+// number as every other block, and its warps share that run's k-tiles evenly,
+// each a contiguous piece of them. A warp's weight stream so runs on from item to
+// item, the rows of X of the block's entries lie in shared memory, and no warp has
+// more to do than another, from one token (an item over six warps) to a full batch
+// (five items a warp). An item that crosses warps is finished by the warp that has
+// its first k-tile, from the other warps' sums in shared memory.
+constexpr int kDWarps = 16;
+constexpr int kDThreads = kDWarps * 32;
+constexpr int kDRows = 32;                      // most rows of X in shared memory
+constexpr int kSums = 8;                        // of a lane for one item
+constexpr size_t kDecodeSmem = 226 * 1024;
+
+constexpr int row_vecs(int K) { return K / 8 + 4; }   // rows 64 bytes apart modulo 128
+constexpr size_t decode_ring_bytes(int group) {
+  return sizeof(uint4) * kDWarps * kStages * stage_vecs(group);
+}
+constexpr size_t decode_fixed_bytes(int group, int E) {
+  return decode_ring_bytes(group) + sizeof(float) * kDWarps * kSums * 32 +
+         sizeof(int) * (2 * (E + 1) + 3 * kDRows + 4);
+}
+// Rows of X that fit beside the rest (at most kDRows).
+int decode_rows(int group, int K, int E) {
+  const size_t fixed = decode_fixed_bytes(group, E);
+  if (fixed >= kDecodeSmem) return 0;
+  return static_cast<int>(std::min<size_t>(kDRows, (kDecodeSmem - fixed) / (sizeof(uint4) * row_vecs(K))));
+}
+
+// The expert of an entry: the last e with first[e] <= entry.
+__device__ __forceinline__ int entry_expert(const int* first, int E, int entry) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= entry) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <bool GATE_UP, int GROUP>
+__global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int cap) {
+  extern __shared__ uint4 smem[];
+  uint4* const ring = smem;
+  uint4* const panel = ring + decode_ring_bytes(GROUP) / sizeof(uint4);           // [cap] rows
+  float* const red = reinterpret_cast<float*>(panel + cap * row_vecs(A.K));       // [warp][kSums][lane]
+  int* const offs = reinterpret_cast<int*>(red + kDWarps * kSums * 32);           // [E + 1]
+  int* const first = offs + A.E + 1;      // [E + 1] first entry of each expert
+  int* const c_expert = first + A.E + 1;  // of each entry at hand: its expert,
+  int* const c_row = c_expert + kDRows;   // its first row,
+  int* const c_at = c_row + kDRows;       // and that row's place in the panel; [count] ends it
+  int* const c_end = c_at + kDRows + 1;   // the first item past the entries at hand
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int kt = A.K / 64;
+  // The down projection's offsets and weights are older than the launch before
+  // it (that launch has waited for all earlier ones), so they are read before the
+  // wait for H. No thread leaves without the wait.
+  if (GATE_UP) pdl_wait();
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e <= A.E; e += kDThreads) offs[e] = min(__ldcg(A.offsets + e), A.M);
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0;
+    for (int base = 0; base < A.E; base += 32) {
+      const int e = base + lane;
+      const int n = e < A.E ? (offs[e + 1] - offs[e] + 7) / 8 : 0;
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (e < A.E) first[e] = carry + x - n;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) first[A.E] = carry;
+  }
+  __syncthreads();
+  const long long total = static_cast<long long>(first[A.E]) * A.nt;
+  const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  int c0 = static_cast<int>(total * blockIdx.x / gridDim.x);
+  bool waited = GATE_UP;
+  Stream<GROUP> stream;
+  while (c0 < end) {
+    // The entries at hand: from item c0 on, as many as the panel holds rows of.
+    const int entry0 = c0 / A.nt;
+    if (threadIdx.x == 0) {
+      int e = entry_expert(first, A.E, entry0), n = 0, at = 0;
+      for (int entry = entry0; n < kDRows && static_cast<long long>(entry) * A.nt < end; ++entry) {
+        while (entry >= first[e + 1]) ++e;
+        const int row = offs[e] + 8 * (entry - first[e]);
+        const int rows = min(offs[e + 1] - row, 8);
+        if (at + rows > cap) break;
+        c_expert[n] = e;
+        c_row[n] = row;
+        c_at[n] = at;
+        at += rows;
+        ++n;
+      }
+      c_at[n] = at;
+      *c_end = static_cast<int>(min(static_cast<long long>(entry0 + n) * A.nt, static_cast<long long>(end)));
+    }
+    __syncthreads();
+    const int c1 = *c_end;
+    const int entries = (c1 - 1) / A.nt - entry0 + 1;
+    // This warp's piece of the items' k-tiles (whole pairs, which groups of 128 need).
+    const int unit = kt & 1 ? 1 : 2;
+    const long long units = static_cast<long long>(c1 - c0) * kt / unit;
+    auto piece = [&](int w) { return static_cast<int>(units * w / kDWarps) * unit; };
+    const int t0 = piece(warp), t1 = piece(warp + 1);
+    int ahead = t0;
+    stream.begin(A.tiles, A.scales, ring + warp * kStages * stage_vecs(GROUP), 0);
+    auto issue = [&]() {
+      if (stream.left <= 0 && ahead < t1) {   // on to the next item's run
+        const int i = ahead / kt, k = ahead - i * kt;
+        const int entry = (c0 + i) / A.nt;
+        const long long tile = static_cast<long long>(c_expert[entry - entry0]) * A.nt + (c0 + i - entry * A.nt);
+        stream.codes = A.tiles + (tile * kt + k) * 64 + lane;
+        stream.scales = A.scales + (tile * (A.K / GROUP) + k * 64 / GROUP) * 4 + lane;
+        stream.left = min(kt - k, t1 - ahead);
+        ahead += stream.left;
+      }
+      stream.issue();
+    };
+    for (int p = 0; p + 1 < kStages; ++p) issue();
+    if (!waited) {
+      pdl_wait();
+      waited = true;
+    }
+    // The entries' rows of X, a warp per row.
+    const int nv = A.K / 8, rows = c_at[entries];
+    for (int j = warp, i = 0; j < rows; j += kDWarps) {
+      while (j >= c_at[i + 1]) ++i;
+      int row = c_row[i] + j - c_at[i];
+      if (GATE_UP && A.perm) row = __ldg(A.perm + row) / A.top_k;
+      if (!index_ok(row >= 0 && row < A.x_rows)) row = 0;
+      const uint4* from = reinterpret_cast<const uint4*>(A.x) + static_cast<long long>(row) * nv;
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(panel + j * row_vecs(A.K)));
+      for (int v = lane; v < nv; v += 32) copy16(to + 16 * v, from + v);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+
+    float acc[2][1][4];
+    int item = 0, run = 0, k = 0;
+    auto finish = [&]() {   // acc is the whole of `item`
+      const int entry = (c0 + item) / A.nt, i = entry - entry0;
+      const int it = c0 + item - entry * A.nt, n = c_at[i + 1] - c_at[i];
+      __nv_bfloat16* const out = A.out + static_cast<long long>(c_row[i]) * A.N;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (2 * c + q >= n) continue;
+        __nv_bfloat16* row = out + static_cast<long long>(2 * c + q) * A.N;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (GATE_UP) {
+            const float G = acc[m][0][q], U = acc[m][0][q + 2];
+            row[16 * it + 8 * m + g] = __float2bfloat16(__fdividef(G, 1.f + __expf(-G)) * U);
+          } else {
+            row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][0][q]);
+            row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][0][q + 2]);
+          }
+        }
+      }
+    };
+    for (int t = t0; t < t1; t += run) {
+      item = t / kt;
+      k = t - item * kt;
+      run = min(kt - k, t1 - t);
+      const int i = (c0 + item) / A.nt - entry0;
+      const int row = c_at[i] + min(g, c_at[i + 1] - c_at[i] - 1);   // past the last row: that row
+      const uint4* xk = panel + row * row_vecs(A.K) + c + 8 * k;
+#pragma unroll
+      for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] = 0.f;
+      for (int left = run; left > 0; left -= kStageTiles) {
+        const int slot = stream.slot + 1 == kStages ? 0 : stream.slot + 1;   // the oldest stage
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();   // its scales are there, and all lanes are done with the last stage
+        issue();
+        const uint4* stage = stream.ring + slot * stage_vecs(GROUP);
+        const uint2* sc = reinterpret_cast<const uint2*>(stage + 64 * kStageTiles) + g;
+#pragma unroll
+        for (int p = 0; p < kStageTiles; ++p) {
+          if (p >= left) break;
+          uint4 x[2][1];
+          x[0][0] = xk[8 * p];
+          x[1][0] = xk[8 * p + 4];
+          one_tile<1, GROUP>(stage + 64 * p + lane, sc + scale_step(GROUP) * p, x, acc);
+        }
+        xk += 8 * kStageTiles;
+      }
+      if (k != 0) {   // the end, or the middle, of an item begun by an earlier warp
+#pragma unroll
+        for (int j = 0; j < kSums; ++j) red[(warp * kSums + j) * 32 + lane] = acc[j / 4][0][j % 4];
+      } else if (run == kt) {
+        finish();
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (t0 < t1 && k == 0 && run < kt) {   // this warp's last item goes on in the next warps
+      int need = kt - run;
+      for (int w = warp + 1; need > 0; ++w) {
+        const int n = min(need, piece(w + 1) - piece(w));
+        if (n > 0) {
+#pragma unroll
+          for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] += red[(w * kSums + j) * 32 + lane];
+        }
+        need -= n;
+      }
+      finish();
+    }
+    c0 = c1;
+    __syncthreads();   // panel, sums and entries are free again
+  }
+  if (!waited) pdl_wait();
+}
+
+template <bool GATE_UP, int S, int NTMAX, int GROUP>
+int launch_kernel(dim3 grid, const W4Args& a, cudaStream_t st) {
+  static_assert(ring_bytes(GROUP) >= sizeof(float) * kWarps * NTMAX * 8 * 32, "sums over the rings");
+  auto kern = w4_kernel<GATE_UP, S, NTMAX, GROUP>;
+  static thread_local int configured = -1;   // the device this thread raised the limit on
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(ring_bytes(GROUP)));
+    if (e != cudaSuccess) {
+      set_last_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    configured = dev;
+  }
+  return launch_pdl(kern, grid, kThreads, ring_bytes(GROUP), st, 1, a);
+}
+
 template <bool GATE_UP, int NTMAX, int GROUP>
 int launch_split(int S, dim3 grid, const W4Args& a, cudaStream_t st) {
-  auto go = [&](auto kern) {
-#if W4_STAGES > 4
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-#endif
-    return launch_pdl(kern, grid, kThreads, ring_bytes(GROUP), st, 1, a);
-  };
-  static_assert(ring_bytes(GROUP) >= sizeof(float) * kWarps * NTMAX * 4 * 32, "sums over the rings");
-  if (S == 1) return go(w4_kernel<GATE_UP, 1, NTMAX, GROUP>);
-  if (S == 2) return go(w4_kernel<GATE_UP, 2, NTMAX, GROUP>);
-  if (S == 4) return go(w4_kernel<GATE_UP, 4, NTMAX, GROUP>);
-  return go(w4_kernel<GATE_UP, 8, NTMAX, GROUP>);
+  if (S == 1) return launch_kernel<GATE_UP, 1, NTMAX, GROUP>(grid, a, st);
+  if (S == 2) return launch_kernel<GATE_UP, 2, NTMAX, GROUP>(grid, a, st);
+  if (S == 4) return launch_kernel<GATE_UP, 4, NTMAX, GROUP>(grid, a, st);
+  return launch_kernel<GATE_UP, 8, NTMAX, GROUP>(grid, a, st);
+}
+
+// Launches the persistent kernel with room for `cap` rows of X.
+template <bool GATE_UP, int GROUP>
+int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
+  auto kern = w4_decode_kernel<GATE_UP, GROUP>;
+  static thread_local int configured = -1;   // the device this thread raised the limit on
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kDecodeSmem));
+    if (e != cudaSuccess) {
+      set_last_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    configured = dev;
+  }
+  const size_t smem = decode_fixed_bytes(GROUP, a.E) + sizeof(uint4) * cap * row_vecs(a.K);
+  return launch_pdl(kern, num_sms(), kDThreads, smem, st, 1, a, cap);
 }
 
 // most_rows: a bound on the rows of one expert.
 template <bool GATE_UP>
 int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st) {
   const int slots = std::min(a.E, a.M);
-  // Split K until the launch has about 24 warps per SM, a warp keeping four tiles at least.
-  const long long want = static_cast<long long>(num_sms()) * 24;
+  const int mean_rows = static_cast<int>(std::min<long long>(most_rows, (static_cast<long long>(a.M) + a.E - 1) / a.E));
+  const long long entries = a.E + a.M / 8;   // at most
+  const int cap = decode_rows(a.group, a.K, a.E);
+  if (mean_rows <= W4_CUT0 && cap >= 8 && entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
+    ProfScope prof(name, st);
+    if (a.group == 32) return launch_decode<GATE_UP, 32>(a, cap, st);
+    if (a.group == 64) return launch_decode<GATE_UP, 64>(a, cap, st);
+    return launch_decode<GATE_UP, 128>(a, cap, st);
+  }
+  // Split K until the launch has about 24 warps per SM three times over, a warp
+  // keeping four k-tiles at least.
+  const long long want = static_cast<long long>(num_sms()) * W4_WANT;
   const long long tiles = static_cast<long long>(slots) * a.nt;
   int S = 1;
   while (S < 8 && tiles * S < want && a.K / 64 >= 8 * S) S *= 2;
@@ -449,9 +771,8 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
     if (a.group == 64) return launch_split<GATE_UP, N, 64>(S, grid, a, st);
     return launch_split<GATE_UP, N, 128>(S, grid, a, st);
   };
-  const int mean = std::min<long long>(most_rows, (a.M + a.E - 1) / a.E);
-  if (mean <= W4_CUT1) return by_group(std::integral_constant<int, 1>());
-  if (mean <= W4_CUT2) return by_group(std::integral_constant<int, 2>());
+  if (mean_rows <= W4_CUT1) return by_group(std::integral_constant<int, 1>());
+  if (mean_rows <= W4_CUT2) return by_group(std::integral_constant<int, 2>());
   return by_group(std::integral_constant<int, 4>());
 }
 
@@ -483,15 +804,15 @@ extern "C" int moe_w4_pack_weights(const uint8_t* codes_a, const moe_bf16* scale
                                    void* stream) {
   using namespace moe;
   if (E < 1 || K < 64 || N < 1 || !group_ok(group) || K % 64 || K % group ||
-      (codes_b == nullptr) != (scales_b == nullptr) || N % (codes_b ? 8 : 16))
+      (codes_b == nullptr) != (scales_b == nullptr) || N % (codes_b ? 16 : 32))
     return MOE_ERR_INVALID_ARG;
   if (!codes_a || !scales_a || !tiles || !scales) return MOE_ERR_INVALID_ARG;
   const void* ptrs[] = {codes_a, scales_a, codes_b, scales_b, tiles, scales};
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_MISALIGNED;
-  const int nt = codes_b ? N / 8 : N / 16, ng = K / group;
-  const long long words = static_cast<long long>(E) * nt * (K / 64) * 128;
-  const long long ns = static_cast<long long>(E) * nt * ng * 16;
+  const int nt = codes_b ? N / 16 : N / 32, ng = K / group;
+  const long long words = static_cast<long long>(E) * nt * (K / 64) * 256;
+  const long long ns = static_cast<long long>(E) * nt * ng * 32;
   if ((words + 255) / 256 > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = as_stream(stream);
   int rc;
@@ -538,7 +859,7 @@ extern "C" int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T,
   a.M = M;
   a.K = d;
   a.N = I;
-  a.nt = I / 8;
+  a.nt = I / 16;
   a.group = group_gu;
   a.x_rows = T;
   const int rc = launch_w4<true>("w4_gate_up", a, perm ? T : M, st);
@@ -550,7 +871,7 @@ extern "C" int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T,
   a.out = reinterpret_cast<__nv_bfloat16*>(y);
   a.K = I;
   a.N = d;
-  a.nt = d / 16;
+  a.nt = d / 32;
   a.group = group_d;
   a.x_rows = M;
   return launch_w4<false>("w4_down", a, perm ? T : M, st);

@@ -625,12 +625,12 @@ int moe_w4_quantize_weights(const moe_bf16* w, int E, int K, int N, int group, u
                             moe_bf16* scales, void* stream);
 
 /* Lays plain weights out for moe_grouped_ffn_w4 (once, when they are loaded): tiles
- * of 16 outputs x 64 K in tensor-core order.
+ * of 32 outputs x 64 K in tensor-core order.
  *   One matrix (the down projection, K = I, N = d): codes_b, scales_b NULL,
- *   N % 16 == 0; tiles [E, N/16, K/64, 512] uint8, scales [E, N/16, K/group, 16] bf16.
+ *   N % 32 == 0; tiles [E, N/32, K/64, 1024] uint8, scales [E, N/32, K/group, 32] bf16.
  *   Gate and up (codes_a, scales_a the gate's, codes_b, scales_b the up
- *   projection's, K = d, N = I): N % 8 == 0; 8 outputs of each share a tile: tiles
- *   [E, N/8, K/64, 512], scales [E, N/8, K/group, 16]. */
+ *   projection's, K = d, N = I): N % 16 == 0; 16 outputs of each share a tile: tiles
+ *   [E, N/16, K/64, 1024], scales [E, N/16, K/group, 32]. */
 int moe_w4_pack_weights(const uint8_t* codes_a, const moe_bf16* scales_a, const uint8_t* codes_b,
                         const moe_bf16* scales_b, int E, int N, int K, int group, uint8_t* tiles,
                         moe_bf16* scales, void* stream);

@@ -80,8 +80,8 @@ def test_w4(lib):
     assert q(OK, 1, 64, 16, 32, MIS, OK, None) == ALIGN
     p = lib.moe_w4_pack_weights
     assert p(OK, OK, OK, None, 1, 16, 64, 32, OK, OK, None) == BAD
-    assert p(OK, OK, None, None, 1, 24, 64, 32, OK, OK, None) == BAD     # N % 16
-    assert p(OK, OK, OK, OK, 1, 12, 64, 32, OK, OK, None) == BAD         # N % 8
+    assert p(OK, OK, None, None, 1, 24, 64, 32, OK, OK, None) == BAD     # N % 32
+    assert p(OK, OK, OK, OK, 1, 12, 64, 32, OK, OK, None) == BAD         # N % 16
     f = lib.moe_grouped_ffn_w4
 
     def call(x=OK, perm=None, T=8, K=1, E=2, M=8, d=128, I=64, gg=64, gd=64, ws=OK, n=1 << 30,

@@ -152,7 +152,7 @@ def test_refusals():
         B.moe_w4_quantize_weights(torch.zeros(1, 128, 8, dtype=BF, device=dev()), 48)
     codes = torch.zeros(1, 12, 64, dtype=torch.uint8, device=dev())
     with pytest.raises(ValueError):
-        B.moe_w4_pack_weights(codes, torch.ones(1, 12, 2, dtype=BF, device=dev()))     # N % 16
+        B.moe_w4_pack_weights(codes, torch.ones(1, 12, 2, dtype=BF, device=dev()))     # N % 32
     with pytest.raises(ValueError):
         B.moe_w4_pack_weights(codes, torch.ones(1, 12, 2, dtype=BF, device=dev()), codes, None)
     with pytest.raises(ValueError):
