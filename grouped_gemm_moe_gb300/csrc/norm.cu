@@ -118,8 +118,8 @@ __device__ __forceinline__ void copies_wait() {   // all but the N newest groups
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// xn = bf16(x r g) over a group's consecutive rows, kStages - 1 of them on their
-// way in shared memory. Each thread reads only the vectors it copied itself, so
+// xn = bf16(x r g) over every workers-th row (the SMs read and write one moving
+// stretch of memory), kStages - 1 rows on their way in shared memory. Each thread reads only the vectors it copied itself, so
 // the ring has no barrier of its own.
 template <int V>
 __global__ void __launch_bounds__(in_threads(V), 1)
@@ -132,9 +132,8 @@ norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain,
   __shared__ __align__(16) float red[64];
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
   const GroupSum group(red, G, grp, lane);
-  const long long worker = static_cast<long long>(blockIdx.x) * (blockDim.x / G) + grp;
-  const int row0 = min(worker * chunk, static_cast<long long>(T));
-  const int row1 = min(static_cast<long long>(row0) + chunk, static_cast<long long>(T));
+  const int workers = gridDim.x * (blockDim.x / G);
+  const int worker = blockIdx.x * (blockDim.x / G) + grp;
   bool has[V];
   float g[V][8];
 #pragma unroll
@@ -146,21 +145,21 @@ norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain,
   auto slot = [&](int stage, int v) {
     return (stage * V + v) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
   };
-  auto issue = [&](int t, int stage) {
+  auto issue = [&](int i) {   // the group's i-th row
+    const long long t = worker + static_cast<long long>(i) * workers;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool live = t < row1 && has[v];
-      copy16(base + 16 * slot(stage, v),
-             x + (live ? static_cast<long long>(t) * nv + lane + v * G : 0), live);
+      const bool live = t < T && has[v];
+      copy16(base + 16 * slot(i % kStages, v), x + (live ? t * nv + lane + v * G : 0), live);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int st = 0; st + 1 < kStages; ++st) issue(row0 + st, st);
+  for (int st = 0; st + 1 < kStages; ++st) issue(st);
   for (int i = 0; i < chunk; ++i) {   // every group of a block runs every step
-    const int t = row0 + i;
+    const long long t = worker + static_cast<long long>(i) * workers;
     copies_wait<kStages - 2>();
-    issue(t + kStages - 1, (i + kStages - 1) % kStages);   // the slot of row t - 1, read by now
+    issue(i + kStages - 1);   // into the slot of row i - 1, read by now
     float f[V][8], s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -169,14 +168,14 @@ norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain,
       for (int q = 0; q < 8; ++q) s = fmaf(f[v][q], f[v][q], s);
     }
     s = group.sum(s, G, i);
-    if (t >= row1) continue;
+    if (t >= T) continue;
     const float r = rsqrtf(s * inv_d + eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!has[v]) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) f[v][q] = f[v][q] * r * g[v][q];
-      stg_v4(xn + static_cast<long long>(t) * nv + lane + v * G, pack8(f[v]));
+      stg_v4(xn + t * nv + lane + v * G, pack8(f[v]));
     }
     if (lane == 0) rstd[t] = r;
   }
@@ -327,7 +326,7 @@ norm_out_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
   }
 }
 
-// The same over a group's consecutive rows, one vector per thread: while a row is
+// The same over every workers-th row, one vector per thread: while a row is
 // combined and normed, the gathered vectors of the next S - 1 rows are on their way
 // into the thread's own slots of shared memory. Lane j of each warp looks up
 // slot j's row and weight a row before they are needed.
@@ -345,9 +344,8 @@ norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
   const GroupSum group(red, G, grp, lane);
   const int wl = threadIdx.x & 31;
-  const long long worker = static_cast<long long>(blockIdx.x) * (blockDim.x / G) + grp;
-  const int row0 = min(worker * chunk, static_cast<long long>(T));
-  const int row1 = min(static_cast<long long>(row0) + chunk, static_cast<long long>(T));
+  const long long workers = gridDim.x * (blockDim.x / G);
+  const long long worker = blockIdx.x * (blockDim.x / G) + grp;
   const bool has = lane < nv;
   const int arrays = K + 1 + (shared_y ? 1 : 0);
   const long long slots = static_cast<long long>(T) * K;
@@ -359,37 +357,35 @@ norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
   auto at = [&](int stage, int array) {
     return (stage * arrays + array) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
   };
-  auto look_up = [&](int t) {   // lane j: the packed row of slot j
-    if (t >= row1 || wl >= K) return 0;
-    const long long a = static_cast<long long>(t) * K + wl;
+  auto look_up = [&](long long t) {   // lane j: the packed row of slot j
+    if (t >= T || wl >= K) return 0;
+    const long long a = t * K + wl;
     const int p = inv_perm ? __ldg(inv_perm + a) : static_cast<int>(a);
     return index_ok(p >= 0 && p < slots) ? p : 0;
   };
-  auto weight = [&](int t) {
-    return (w && t < row1 && wl < K) ? __ldg(w + static_cast<long long>(t) * K + wl) : 1.f;
-  };
-  auto issue = [&](int t, int stage, int pos) {
-    const bool live = t < row1 && has;
+  auto weight = [&](long long t) { return (w && t < T && wl < K) ? __ldg(w + t * K + wl) : 1.f; };
+  auto issue = [&](long long t, int stage, int pos) {
+    const bool live = t < T && has;
     for (int j = 0; j < K; ++j) {
       const long long p = __shfl_sync(0xffffffffu, pos, j);
       copy16(base + 16 * at(stage, j), y + (live ? p * nv + lane : 0), live);
     }
-    const long long own = live ? static_cast<long long>(t) * nv + lane : 0;
+    const long long own = live ? t * nv + lane : 0;
     copy16(base + 16 * at(stage, K), resid + own, live);
     if (shared_y) copy16(base + 16 * at(stage, K + 1), shared_y + own, live);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int st = 0; st + 1 < S; ++st) issue(row0 + st, st, look_up(row0 + st));
-  int pos = look_up(row0 + S - 1);
-  float wt = weight(row0);
+  for (int st = 0; st + 1 < S; ++st) issue(worker + st * workers, st, look_up(worker + st * workers));
+  int pos = look_up(worker + (S - 1) * workers);
+  float wt = weight(worker);
   for (int i = 0; i < chunk; ++i) {   // every group of a block runs every step
-    const int t = row0 + i;
-    const bool live = t < row1;
+    const long long t = worker + i * workers;
+    const bool live = t < T;
     copies_wait<S - 2>();
-    issue(t + S - 1, (i + S - 1) % S, pos);   // the slots of row t - 1, read by now
-    pos = look_up(t + S);
-    const float next_wt = weight(t + 1);
+    issue(t + (S - 1) * workers, (i + S - 1) % S, pos);   // the slots of the last row, read by now
+    pos = look_up(t + S * workers);
+    const float next_wt = weight(t + workers);
     const int stage = i % S;
     float z[8];
 #pragma unroll
@@ -408,7 +404,7 @@ norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
 #pragma unroll
       for (int q = 0; q < 8; ++q) z[q] += f[q];
     }
-    const long long own = static_cast<long long>(t) * nv + lane;
+    const long long own = t * nv + lane;
     if (zsum && live && has) stg_v4(zsum + own, pack8(z));
     float r = 1.f;
     if (gain) {

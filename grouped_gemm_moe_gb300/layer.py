@@ -15,6 +15,13 @@ fractions, mean router probabilities, the load-balance loss and load metrics,
 in lb_frac / lb_pmean / lb_stats) and the backward adds aux_loss_coef times
 the loss's gradient into dlogits with moe_load_balance_backward.
 
+With ckpt8 the layer keeps what its backward needs of the activations as 8-bit
+checkpoints (x, [G | U] and y; H is made again) and takes its large buffers
+from a LayerScratch that the layers of a model share:
+Forward:  ... -> moe_ckpt8_pack of x, [G | U] and y -> moe_combine.
+Backward: moe_ckpt8_combine_backward -> moe_ckpt8_dispatch -> moe_ckpt8_swiglu
+          -> the steps above from moe_grouped_ffn_backward_data on.
+
 This module only allocates tensors and orders the calls; each step is a
 kernel of libmoe_gb300.so.
 """
@@ -27,10 +34,30 @@ import torch
 from . import binding as B
 
 
+class LayerScratch:
+    """The buffers of a layer that hold nothing between its calls when it keeps
+    8-bit checkpoints: one of these serves all layers of one shape that run on one
+    stream."""
+
+    def __init__(self, T: int, d: int, E: int, K: int, I: int, shared_I: int = 0, device=None):
+        self.shape = (T, d, E, K, I, shared_I)
+        TK, bf = T * K, torch.bfloat16
+        e = lambda *s: torch.empty(*s, dtype=bf, device=device)  # noqa: E731
+        self.xp, self.y, self.h, self.gu = e(TK, d), e(TK, d), e(TK, I), e(TK, 2 * I)
+        self.dy, self.dxp = e(TK, d), e(TK, d)
+        self.ws_ffn = B.new_workspace(B.workspace_size(B.MOE_OP_GROUPED_FFN, T, E, K, 1, d, I), device)
+        self.ws_bwd = B.new_workspace(
+            B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, E, K, 1, d, I), device)
+        if shared_I:
+            self.xs, self.ys, self.dxs = e(T, d), e(T, d), e(T, d)
+            self.hs, self.gus = e(T, shared_I), e(T, 2 * shared_I)
+
+
 class MoELayer:
     def __init__(self, T: int, d: int, E: int, K: int, I: int, R: int,
                  weights: Dict[str, torch.Tensor], renorm: int = 1,
-                 device: Optional[torch.device] = None, aux_loss_coef: float = 0.0):
+                 device: Optional[torch.device] = None, aux_loss_coef: float = 0.0,
+                 ckpt8: bool = False, scratch: Optional[LayerScratch] = None):
         self.T, self.d, self.E, self.K, self.I, self.R = T, d, E, K, I, R
         self.renorm = renorm
         dev = torch.device(device) if device is not None else weights["w_gate"].device
@@ -48,19 +75,42 @@ class MoELayer:
         self.ep_splits = e(n_split, dt=i32)
         self.send_index, self.a2a_index, self.regroup_index = (e(TK, dt=i32) for _ in range(3))
         self.host_splits = torch.empty(n_split, dtype=i32, pin_memory=True)
-        self.xp = e(TK, d, dt=bf)
-        self.y, self.h, self.gu = e(TK, d, dt=bf), e(TK, I, dt=bf), e(TK, 2 * I, dt=bf)
+        self.ckpt8 = bool(ckpt8)
+        shared_I = weights["ws_gate"].shape[1] if self.shared else 0
+        if scratch is not None:
+            if not ckpt8:
+                raise ValueError("a shared scratch needs ckpt8: without checkpoints its buffers "
+                                 "hold the layer's saved activations")
+            if scratch.shape != (T, d, E, K, I, shared_I):
+                raise ValueError(f"scratch of {scratch.shape} for {(T, d, E, K, I, shared_I)}")
+        elif ckpt8:
+            scratch = LayerScratch(T, d, E, K, I, shared_I, dev)
+        self.scratch = scratch
+        if scratch is not None:
+            self.xp, self.y, self.h, self.gu = scratch.xp, scratch.y, scratch.h, scratch.gu
+            kept = lambda M, N: (torch.empty(M, N, dtype=torch.int8, device=dev),  # noqa: E731
+                                 e(M, -(-N // 32), dt=bf))
+            self.x8, self.gu8, self.y8 = kept(T, d), kept(TK, 2 * I), kept(TK, d)
+            self.gus8 = kept(T, 2 * shared_I) if self.shared else None
+        else:
+            self.xp = e(TK, d, dt=bf)
+            self.y, self.h, self.gu = e(TK, d, dt=bf), e(TK, I, dt=bf), e(TK, 2 * I, dt=bf)
         self.out = e(T, d, dt=bf)
         self.ws_ep = B.new_workspace(B.workspace_size(B.MOE_OP_ROUTE_PERMUTE_EP, T, E, K, R), dev)
-        self.ws_ffn = B.new_workspace(B.workspace_size(B.MOE_OP_GROUPED_FFN, T, E, K, 1, d, I), dev)
-        # backward buffers
-        self.dy, self.dtopk_w = e(TK, d, dt=bf), e(T, K, dt=f32)
-        self.dxp = e(TK, d, dt=bf)
+        self.dtopk_w = e(T, K, dt=f32)
+        # forward workspace and backward buffers
+        if scratch is not None:
+            self.ws_ffn, self.ws_bwd = scratch.ws_ffn, scratch.ws_bwd
+            self.dy, self.dxp = scratch.dy, scratch.dxp
+        else:
+            self.ws_ffn = B.new_workspace(
+                B.workspace_size(B.MOE_OP_GROUPED_FFN, T, E, K, 1, d, I), dev)
+            self.dy, self.dxp = e(TK, d, dt=bf), e(TK, d, dt=bf)
+            self.ws_bwd = B.new_workspace(
+                B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, E, K, 1, d, I), dev)
         self.dw_gate, self.dw_up = e(E, d, I, dt=f32), e(E, d, I, dt=f32)
         self.dw_down = e(E, I, d, dt=f32)
         self.dx, self.dlogits = e(T, d, dt=bf), e(T, E, dt=f32)
-        self.ws_bwd = B.new_workspace(
-            B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, E, K, 1, d, I), dev)
         if self.shared:
             Is = weights["ws_gate"].shape[1]
             self.Is = Is
@@ -68,8 +118,12 @@ class MoELayer:
             self.ws_u = weights["ws_up"].unsqueeze(0)
             self.ws_d = weights["ws_down"].unsqueeze(0)
             self.s_offsets = torch.tensor([0, T], dtype=i32, device=dev)
-            self.ys, self.hs, self.gus = e(T, d, dt=bf), e(T, Is, dt=bf), e(T, 2 * Is, dt=bf)
-            self.dxs = e(T, d, dt=bf)
+            if scratch is not None:
+                self.ys, self.hs, self.gus = scratch.ys, scratch.hs, scratch.gus
+                self.dxs = scratch.dxs
+            else:
+                self.ys, self.hs, self.gus = e(T, d, dt=bf), e(T, Is, dt=bf), e(T, 2 * Is, dt=bf)
+                self.dxs = e(T, d, dt=bf)
             self.dws_gate, self.dws_up = e(1, d, Is, dt=f32), e(1, d, Is, dt=f32)
             self.dws_down = e(1, Is, d, dt=f32)
             self.ws_sfwd = B.new_workspace(B.workspace_size(B.MOE_OP_GROUPED_FFN, T, 1, 1, 1, d, Is), dev)
@@ -108,6 +162,13 @@ class MoELayer:
 
     # -------------------------------------------------------------- passes
     def forward(self, logits: torch.Tensor, x: torch.Tensor, copy_splits: bool = True):
+        y, topk_w, inv_perm, shared_y = self.experts(logits, x, copy_splits)
+        self._run("combine", B.moe_combine, y, topk_w, inv_perm, shared_y, out=self.out)
+        return self.out
+
+    def experts(self, logits: torch.Tensor, x: torch.Tensor, copy_splits: bool = True):
+        """The forward up to its combine, for a caller that fuses the combine with what
+        follows (moe_norm_out): returns that call's (y, topk_w, inv_perm, shared_y)."""
         self.logits, self.x = logits, x
         w = self.w
         K, E, R = self.K, self.E, self.R
@@ -130,14 +191,32 @@ class MoELayer:
             self._run("shared_ffn", B.moe_grouped_ffn, x, self.s_offsets, self.ws_g, self.ws_u,
                       self.ws_d, ws=self.ws_sfwd, out=(self.ys, self.hs, self.gus))
             shared_y = self.ys
-        self._run("combine", B.moe_combine, self.y, self.topk_w, self.inv_perm, shared_y,
-                  out=self.out)
-        return self.out
+        if self.ckpt8:
+            self._run("ckpt8_x", B.moe_ckpt8_pack, x, out=self.x8)
+            self._run("ckpt8_gu", B.moe_ckpt8_pack, self.gu, out=self.gu8)
+            self._run("ckpt8_y", B.moe_ckpt8_pack, self.y, out=self.y8)
+            if self.shared:
+                self._run("ckpt8_shared_gu", B.moe_ckpt8_pack, self.gus, out=self.gus8)
+            self.x = None       # the backward restores it
+        return self.y, self.topk_w, self.inv_perm, shared_y
 
     def backward(self, dout: torch.Tensor):
         w = self.w
-        self._run("combine_backward", B.moe_combine_backward, dout, self.y, self.topk_w,
-                  self.inv_perm, out=(self.dy, self.dtopk_w))
+        x = self.x
+        if self.ckpt8:
+            self._run("combine_backward", B.moe_ckpt8_combine_backward, dout, *self.y8, self.topk_w,
+                      self.inv_perm, out=(self.dy, self.dtopk_w))
+            self._run("ckpt8_dispatch", B.moe_ckpt8_dispatch, *self.x8, self.inv_perm, self.K,
+                      out=self.xp)
+            self._run("ckpt8_swiglu", B.moe_ckpt8_swiglu, *self.gu8, out=(self.gu, self.h))
+            if self.shared:
+                x = self.scratch.xs
+                self._run("ckpt8_restore", B.moe_ckpt8_dispatch, *self.x8, out=x)
+                self._run("ckpt8_shared_swiglu", B.moe_ckpt8_swiglu, *self.gus8,
+                          out=(self.gus, self.hs))
+        else:
+            self._run("combine_backward", B.moe_combine_backward, dout, self.y, self.topk_w,
+                      self.inv_perm, out=(self.dy, self.dtopk_w))
         # data parts first, then the gather of dx while the GEMMs' dX rows are still
         # in L2, then the weight gradients
         self._run("grouped_ffn_backward_data", B.moe_grouped_ffn_backward_data, self.dy, self.xp,
@@ -145,7 +224,7 @@ class MoELayer:
                   ws=self.ws_bwd, out=self.dxp)
         dxs = None
         if self.shared:
-            self._run("shared_ffn_backward_data", B.moe_grouped_ffn_backward_data, dout, self.x,
+            self._run("shared_ffn_backward_data", B.moe_grouped_ffn_backward_data, dout, x,
                       self.gus, self.hs, self.s_offsets, self.ws_g, self.ws_u, self.ws_d,
                       ws=self.ws_sbwd, out=self.dxs)
             dxs = self.dxs
@@ -156,7 +235,7 @@ class MoELayer:
                   out=(self.dw_gate, self.dw_up, self.dw_down))
         if self.shared:
             self._run("shared_ffn_backward_weights", B.moe_grouped_ffn_backward_weights, dout,
-                      self.x, self.hs, self.s_offsets, 1, self.Is, ws=self.ws_sbwd,
+                      x, self.hs, self.s_offsets, 1, self.Is, ws=self.ws_sbwd,
                       out=(self.dws_gate, self.dws_up, self.dws_down))
         self._run("route_topk_backward", B.moe_route_topk_backward,
                   None if self.renorm else self.logits, self.topk_idx, self.topk_w, self.dtopk_w,
@@ -301,9 +380,10 @@ class MoELayer:
 
 
 def layer_from_config(cfg, inputs: Dict[str, torch.Tensor], device,
-                      aux_loss_coef: float = 0.0) -> MoELayer:
+                      aux_loss_coef: float = 0.0, ckpt8: bool = False,
+                      scratch: Optional[LayerScratch] = None) -> MoELayer:
     """Copies a workload's weights to ``device`` and builds the layer."""
     keys = ["w_gate", "w_up", "w_down"] + (["ws_gate", "ws_up", "ws_down"] if cfg.shared_I else [])
     weights = {k: inputs[k].to(device).contiguous() for k in keys}
     return MoELayer(cfg.T, cfg.d, cfg.E, cfg.K, cfg.I, cfg.R, weights, cfg.renorm, device,
-                    aux_loss_coef)
+                    aux_loss_coef, ckpt8, scratch)
