@@ -34,6 +34,9 @@ namespace {
 #ifndef W4_BLK
 #define W4_BLK 3
 #endif
+#ifndef W4_MIN
+#define W4_MIN 20000
+#endif
 #ifndef W4_CUT0
 #define W4_CUT0 8
 #endif
@@ -164,15 +167,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The same into a fresh sum.
-__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // A product into d from the sums c.
 __device__ __forceinline__ void mma16816_from(float (&d)[4], const float (&c)[4],
                                               const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -192,41 +186,45 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], float s0, float s1, 
 
 // Half a tile (32 K) against 8 NT rows of X, scaled into acc[16 outputs][rows].
 // w: the lane's words of rows g and g + 8 in each 16 outputs; sc its four scales.
-// The codes come as 128 + q. With 8 rows two products by the constant -136
-// start the sums of both 16 outputs and take the excess out again (fp32 sums of
-// exact products, an error of about 2^-19 of the result), on tensor cores that
-// are mostly idle; with more rows those products would multiply, and the exact
-// subtractions that all rows share are the cheaper way.
 template <int NT>
 __device__ __forceinline__ void half_tile(uint32_t w00, uint32_t w01, uint32_t w10, uint32_t w11,
                                           const uint4 (&x)[NT], uint2 sc, float (&acc)[2][NT][4]) {
   const float s[2][2] = {{bf16_lo(sc.x), bf16_hi(sc.x)}, {bf16_lo(sc.y), bf16_hi(sc.y)}};
-  float less[4];
-  if (NT == 1) {
-    const uint32_t c[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
-    mma16816_first(less, c, x[0].x, x[0].y);
-    mma16816(less, c, x[0].z, x[0].w);
-  }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const uint32_t w0 = m ? w10 : w00, w1 = m ? w11 : w01;
-    uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
-    uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
-    if (NT > 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a0[i] = centred(a0[i]);
-        a1[i] = centred(a1[i]);
-      }
-    }
+    const uint32_t a0[4] = {centred(pair_of(w0, 0)), centred(pair_of(w1, 0)),
+                            centred(pair_of(w0, 1)), centred(pair_of(w1, 1))};
+    const uint32_t a1[4] = {centred(pair_of(w0, 2)), centred(pair_of(w1, 2)),
+                            centred(pair_of(w0, 3)), centred(pair_of(w1, 3))};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
       float p[4];
-      if (NT == 1) mma16816_from(p, less, a0, x[n].x, x[n].y);
-      else mma16816_first(p, a0, x[n].x, x[n].y);
+      mma16816_from(p, zero, a0, x[n].x, x[n].y);
       mma16816(p, a1, x[n].z, x[n].w);
       add_scaled(acc[m][n], s[m][0], s[m][1], p);
     }
+  }
+}
+
+// The same against 8 rows without the subtractions: the codes stay 128 + q, and
+// the sums start from less = -136 sum x of the half for the lane's two rows (fp32;
+// what the cancellation leaves is an error of about 2^-19 of the result).
+__device__ __forceinline__ void half_tile_less(uint32_t w00, uint32_t w01, uint32_t w10,
+                                               uint32_t w11, const uint4& x, float2 less, uint2 sc,
+                                               float (&acc)[2][4]) {
+  const float s[2][2] = {{bf16_lo(sc.x), bf16_hi(sc.x)}, {bf16_lo(sc.y), bf16_hi(sc.y)}};
+  const float start[4] = {less.x, less.y, less.x, less.y};
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t w0 = m ? w10 : w00, w1 = m ? w11 : w01;
+    const uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
+    const uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
+    float p[4];
+    mma16816_from(p, start, a0, x.x, x.y);
+    mma16816(p, a1, x.z, x.w);
+    add_scaled(acc[m], s[m][0], s[m][1], p);
   }
 }
 
@@ -496,15 +494,18 @@ constexpr int row_vecs(int K) { return K / 8 + 4; }   // rows 64 bytes apart mod
 constexpr size_t decode_ring_bytes(int group) {
   return sizeof(uint4) * kDWarps * kStages * stage_vecs(group);
 }
+constexpr size_t decode_row_bytes(int K) {   // a row of X and its sums over 32 K
+  return sizeof(uint4) * row_vecs(K) + sizeof(float) * (K / 32);
+}
 constexpr size_t decode_fixed_bytes(int group, int E) {
   return decode_ring_bytes(group) + sizeof(float) * kDWarps * kSums * 32 +
-         sizeof(int) * (2 * (E + 1) + 3 * kDRows + 4);
+         sizeof(int) * (2 * (E + 1) + 4 * kDRows + 4);
 }
-// Rows of X that fit beside the rest (at most kDRows).
+// Rows of X that fit beside the rest (an even number, at most kDRows).
 int decode_rows(int group, int K, int E) {
   const size_t fixed = decode_fixed_bytes(group, E);
   if (fixed >= kDecodeSmem) return 0;
-  return static_cast<int>(std::min<size_t>(kDRows, (kDecodeSmem - fixed) / (sizeof(uint4) * row_vecs(K))));
+  return static_cast<int>(std::min<size_t>(kDRows, (kDecodeSmem - fixed) / decode_row_bytes(K))) & ~1;
 }
 
 // The expert of an entry: the last e with first[e] <= entry.
@@ -523,11 +524,13 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
   uint4* const ring = smem;
   uint4* const panel = ring + decode_ring_bytes(GROUP) / sizeof(uint4);           // [cap] rows
   float* const red = reinterpret_cast<float*>(panel + cap * row_vecs(A.K));       // [warp][kSums][lane]
-  int* const offs = reinterpret_cast<int*>(red + kDWarps * kSums * 32);           // [E + 1]
+  float* const less = red + kDWarps * kSums * 32;   // [K / 32][cap]: -136 times a row's sums
+  int* const offs = reinterpret_cast<int*>(less + cap * (A.K / 32));   // [E + 1]
   int* const first = offs + A.E + 1;      // [E + 1] first entry of each expert
   int* const c_expert = first + A.E + 1;  // of each entry at hand: its expert,
   int* const c_row = c_expert + kDRows;   // its first row,
-  int* const c_at = c_row + kDRows;       // and that row's place in the panel; [count] ends it
+  int* const c_rows = c_row + kDRows;     // its rows,
+  int* const c_at = c_rows + kDRows;      // their (even) place in the panel; [count] ends it
   int* const c_end = c_at + kDRows + 1;   // the first item past the entries at hand
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -573,8 +576,9 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
         if (at + rows > cap) break;
         c_expert[n] = e;
         c_row[n] = row;
+        c_rows[n] = rows;
         c_at[n] = at;
-        at += rows;
+        at += (rows + 1) & ~1;
         ++n;
       }
       c_at[n] = at;
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
     const int nv = A.K / 8, rows = c_at[entries];
     for (int j = warp, i = 0; j < rows; j += kDWarps) {
       while (j >= c_at[i + 1]) ++i;
-      int row = c_row[i] + j - c_at[i];
+      int row = c_row[i] + min(j - c_at[i], c_rows[i] - 1);
       if (GATE_UP && A.perm) row = __ldg(A.perm + row) / A.top_k;
       if (!index_ok(row >= 0 && row < A.x_rows)) row = 0;
       const uint4* from = reinterpret_cast<const uint4*>(A.x) + static_cast<long long>(row) * nv;
@@ -621,12 +625,26 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
+    const int kg = A.K / 32;
+    for (int j = threadIdx.x; j < rows * kg; j += kDThreads) {
+      const int h = j / rows, r = j - h * rows;   // neighbouring threads in different rows' banks
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float f[8];
+        unpack8(panel[r * row_vecs(A.K) + 4 * h + v], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum += f[q];
+      }
+      less[h * cap + r] = -136.f * sum;
+    }
+    __syncthreads();
 
-    float acc[2][1][4];
+    float acc[2][4];
     int item = 0, run = 0, k = 0;
     auto finish = [&]() {   // acc is the whole of `item`
       const int entry = (c0 + item) / A.nt, i = entry - entry0;
-      const int it = c0 + item - entry * A.nt, n = c_at[i + 1] - c_at[i];
+      const int it = c0 + item - entry * A.nt, n = c_rows[i];
       __nv_bfloat16* const out = A.out + static_cast<long long>(c_row[i]) * A.N;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -635,11 +653,11 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (GATE_UP) {
-            const float G = acc[m][0][q], U = acc[m][0][q + 2];
+            const float G = acc[m][q], U = acc[m][q + 2];
             row[16 * it + 8 * m + g] = __float2bfloat16(__fdividef(G, 1.f + __expf(-G)) * U);
           } else {
-            row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][0][q]);
-            row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][0][q + 2]);
+            row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][q]);
+            row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][q + 2]);
           }
         }
       }
@@ -649,10 +667,12 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
       k = t - item * kt;
       run = min(kt - k, t1 - t);
       const int i = (c0 + item) / A.nt - entry0;
-      const int row = c_at[i] + min(g, c_at[i + 1] - c_at[i] - 1);   // past the last row: that row
+      const int row = c_at[i] + min(g, c_rows[i] - 1);   // past the last row: that row
       const uint4* xk = panel + row * row_vecs(A.K) + c + 8 * k;
+      // the lane's two rows (within the panel's places even past the last row)
+      const float* lk = less + 2 * k * cap + min(c_at[i] + 2 * c, cap - 2);
 #pragma unroll
-      for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] = 0.f;
+      for (int j = 0; j < kSums; ++j) acc[j / 4][j % 4] = 0.f;
       for (int left = run; left > 0; left -= kStageTiles) {
         const int slot = stream.slot + 1 == kStages ? 0 : stream.slot + 1;   // the oldest stage
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -663,16 +683,20 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
 #pragma unroll
         for (int p = 0; p < kStageTiles; ++p) {
           if (p >= left) break;
-          uint4 x[2][1];
-          x[0][0] = xk[8 * p];
-          x[1][0] = xk[8 * p + 4];
-          one_tile<1, GROUP>(stage + 64 * p + lane, sc + scale_step(GROUP) * p, x, acc);
+          const uint4 a = stage[64 * p + lane], b = stage[64 * p + 32 + lane];
+          const uint2 s0 = sc[scale_step(GROUP) * p];
+          const uint2 s1 = GROUP == 32 ? sc[scale_step(GROUP) * p + 8] : s0;
+          half_tile_less(a.x, a.y, b.x, b.y, xk[8 * p],
+                         *reinterpret_cast<const float2*>(lk + 2 * p * cap), s0, acc);
+          half_tile_less(a.z, a.w, b.z, b.w, xk[8 * p + 4],
+                         *reinterpret_cast<const float2*>(lk + (2 * p + 1) * cap), s1, acc);
         }
         xk += 8 * kStageTiles;
+        lk += 2 * kStageTiles * cap;
       }
       if (k != 0) {   // the end, or the middle, of an item begun by an earlier warp
 #pragma unroll
-        for (int j = 0; j < kSums; ++j) red[(warp * kSums + j) * 32 + lane] = acc[j / 4][0][j % 4];
+        for (int j = 0; j < kSums; ++j) red[(warp * kSums + j) * 32 + lane] = acc[j / 4][j % 4];
       } else if (run == kt) {
         finish();
       }
@@ -685,7 +709,7 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
         const int n = min(need, piece(w + 1) - piece(w));
         if (n > 0) {
 #pragma unroll
-          for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] += red[(w * kSums + j) * 32 + lane];
+          for (int j = 0; j < kSums; ++j) acc[j / 4][j % 4] += red[(w * kSums + j) * 32 + lane];
         }
         need -= n;
       }
@@ -740,7 +764,7 @@ int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
     }
     configured = dev;
   }
-  const size_t smem = decode_fixed_bytes(GROUP, a.E) + sizeof(uint4) * cap * row_vecs(a.K);
+  const size_t smem = decode_fixed_bytes(GROUP, a.E) + cap * decode_row_bytes(a.K);
   return launch_pdl(kern, num_sms(), kDThreads, smem, st, 1, a, cap);
 }
 
@@ -751,7 +775,8 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
   const int mean_rows = static_cast<int>(std::min<long long>(most_rows, (static_cast<long long>(a.M) + a.E - 1) / a.E));
   const long long entries = a.E + a.M / 8;   // at most
   const int cap = decode_rows(a.group, a.K, a.E);
-  if (mean_rows <= W4_CUT0 && cap >= 8 && entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
+  const long long k_tiles = static_cast<long long>(slots) * a.nt * (a.K / 64);
+  if (mean_rows <= W4_CUT0 && k_tiles >= W4_MIN && cap >= 8 && entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
     ProfScope prof(name, st);
     if (a.group == 32) return launch_decode<GATE_UP, 32>(a, cap, st);
     if (a.group == 64) return launch_decode<GATE_UP, 64>(a, cap, st);
