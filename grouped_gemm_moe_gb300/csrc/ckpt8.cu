@@ -152,6 +152,88 @@ __device__ __forceinline__ __nv_bfloat162 abs2(uint32_t v) {
   return *reinterpret_cast<__nv_bfloat162*>(&v);
 }
 
+// Codes and scales of a thread's kPackUnroll units. The four lanes of a block of 32
+// call it together; put(i, codes, scale) stores unit i.
+template <typename Put>
+__device__ __forceinline__ void pack_units(const uint4 (&raw)[kPackUnroll], Put put) {
+  // The magnitude's maximum over each block, in pairs, NaN and infinity kept.
+  float amax[kPackUnroll];
+#pragma unroll
+  for (int i = 0; i < kPackUnroll; ++i) {
+    __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(abs2(raw[i].x), abs2(raw[i].y)),
+                                   __hmax2_nan(abs2(raw[i].z), abs2(raw[i].w)));
+    m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    amax[i] = __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+  }
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < kPackUnroll; ++i) fine = fine && amax[i] < INFINITY;
+  if (!__all_sync(0xffffffffu, fine)) {   // rare: the maximum over the finite values instead
+#pragma unroll
+    for (int i = 0; i < kPackUnroll; ++i) {
+      float f[8], top = 0.f;
+      unpack8(raw[i], f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fabsf(f[k]) < INFINITY ? fmaxf(top, fabsf(f[k])) : top;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      amax[i] = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    }
+  }
+  // Lane l of a block's four works out the scale and reciprocal of unit l.
+  static_assert(kPackUnroll == 4, "one unit per lane of a block");
+  const int l = threadIdx.x & 3;
+  const float mine = l == 0 ? amax[0] : l == 1 ? amax[1] : l == 2 ? amax[2] : amax[3];
+  const float my_scale = block_scale(mine);
+  const float my_inv = __frcp_rn(my_scale);
+#pragma unroll
+  for (int i = 0; i < kPackUnroll; ++i) {
+    const float r = __shfl_sync(0xffffffffu, my_inv, i, 4);
+    const float sc = __shfl_sync(0xffffffffu, my_scale, i, 4);
+    float f[8];
+    unpack8(raw[i], f);
+    uint2 c = make_uint2(encode4(f, r), encode4(f + 4, r));
+    if (!fine) c = make_uint2(mark4(c.x, f), mark4(c.y, f + 4));
+    put(i, c, static_cast<uint16_t>(__float_as_uint(sc) >> 16));
+  }
+}
+
+// Rows of whole blocks (N % 32 == 0): units, codes and scales are flat arrays, and
+// only the last tile of a call has edges. The row arithmetic and edge checks of
+// the other form cost it a quarter of its time, on the logic pipe that both wait for.
+__global__ void __launch_bounds__(kThreads)
+pack_flat_kernel(const uint4* __restrict__ x, long long total, uint2* __restrict__ q,
+                 uint16_t* __restrict__ s) {
+  pdl_enter();
+  constexpr int kTile = kThreads * kPackUnroll;
+  for (long long base = static_cast<long long>(blockIdx.x) * kTile; base < total;
+       base += static_cast<long long>(gridDim.x) * kTile) {
+    const uint4* xt = x + base + threadIdx.x;
+    uint2* qt = q + base + threadIdx.x;
+    uint16_t* st = s + base / 4 + threadIdx.x / 4;
+    uint4 raw[kPackUnroll];
+    const bool lead = (threadIdx.x & 3) == 0;
+    if (base + kTile <= total) {
+#pragma unroll
+      for (int i = 0; i < kPackUnroll; ++i) raw[i] = ldg_nc_v4(xt + i * kThreads);
+      pack_units(raw, [&](int i, uint2 c, uint16_t sc) {
+        qt[i * kThreads] = c;
+        if (lead) st[i * (kThreads / 4)] = sc;
+      });
+    } else {
+      const int left = static_cast<int>(total - base) - static_cast<int>(threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < kPackUnroll; ++i)
+        raw[i] = i * kThreads < left ? ldg_nc_v4(xt + i * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+      pack_units(raw, [&](int i, uint2 c, uint16_t sc) {
+        if (i * kThreads >= left) return;
+        qt[i * kThreads] = c;
+        if (lead) st[i * (kThreads / 4)] = sc;
+      });
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads)
 pack_kernel(const uint4* __restrict__ x, Tiles tl, int nv, uint2* __restrict__ q,
             uint16_t* __restrict__ s) {
@@ -172,50 +254,11 @@ pack_kernel(const uint4* __restrict__ x, Tiles tl, int nv, uint2* __restrict__ q
         raw[i] = row[i] >= 0 ? ldg_nc_v4(x + (row0 + row[i]) * nv + col[i])
                              : make_uint4(0u, 0u, 0u, 0u);
       }
-      // The magnitude's maximum over each block, in pairs, NaN and infinity kept.
-      float amax[kPackUnroll];
-#pragma unroll
-      for (int i = 0; i < kPackUnroll; ++i) {
-        __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(abs2(raw[i].x), abs2(raw[i].y)),
-                                       __hmax2_nan(abs2(raw[i].z), abs2(raw[i].w)));
-        m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        amax[i] = __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
-      }
-      bool fine = true;
-#pragma unroll
-      for (int i = 0; i < kPackUnroll; ++i) fine = fine && amax[i] < INFINITY;
-      if (!__all_sync(0xffffffffu, fine)) {   // rare: the maximum over the finite values instead
-#pragma unroll
-        for (int i = 0; i < kPackUnroll; ++i) {
-          float f[8], top = 0.f;
-          unpack8(raw[i], f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) top = fabsf(f[k]) < INFINITY ? fmaxf(top, fabsf(f[k])) : top;
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          amax[i] = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        }
-      }
-      // Lane l of a block's four works out the scale and reciprocal of unit l.
-      static_assert(kPackUnroll == 4, "one unit per lane of a block");
-      const int l = threadIdx.x & 3;
-      const float mine = l == 0 ? amax[0] : l == 1 ? amax[1] : l == 2 ? amax[2] : amax[3];
-      const float my_scale = block_scale(mine);
-      const float my_inv = __frcp_rn(my_scale);
-#pragma unroll
-      for (int i = 0; i < kPackUnroll; ++i) {
-        const float r = __shfl_sync(0xffffffffu, my_inv, i, 4);
-        const float sc = __shfl_sync(0xffffffffu, my_scale, i, 4);
-        if (row[i] < 0) continue;
-        float f[8];
-        unpack8(raw[i], f);
-        uint2 c = make_uint2(encode4(f, r), encode4(f + 4, r));
-        if (!fine) c = make_uint2(mark4(c.x, f), mark4(c.y, f + 4));
+      pack_units(raw, [&](int i, uint2 c, uint16_t sc) {
+        if (row[i] < 0) return;
         q[(row0 + row[i]) * nv + col[i]] = c;
-        if ((col[i] & 3) == 0)
-          s[(row0 + row[i]) * (tl.per_row / 4) + col[i] / 4] =
-              static_cast<uint16_t>(__float_as_uint(sc) >> 16);
-      }
+        if ((col[i] & 3) == 0) s[(row0 + row[i]) * (tl.per_row / 4) + col[i] / 4] = sc;
+      });
     }
   }
 }
@@ -321,7 +364,6 @@ combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict
   if (!index_ok(my_row >= 0 && my_row < T * K)) my_row = -1;   // debug builds: skipped, dw 0
   float my_dot = 0.f;
   for (int c0 = lane; c0 - lane < nv; c0 += 32 * kCbVecs) {
-    uint4 dv[kCbVecs];
     uint2 yv[kCbVecs];
     uint16_t sv[kCbVecs];
     auto load = [&](int j) {
@@ -338,10 +380,11 @@ combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict
       }
     };
     load(0);
+    float fd[kCbVecs][8];
 #pragma unroll
     for (int u = 0; u < kCbVecs; ++u) {
       const int c = c0 + 32 * u;
-      dv[u] = c < nv ? ldg_nc_v4(dout + t * nv + c) : make_uint4(0u, 0u, 0u, 0u);
+      unpack8(c < nv ? ldg_nc_v4(dout + t * nv + c) : make_uint4(0u, 0u, 0u, 0u), fd[u]);
     }
     for (int j = 0; j < K; ++j) {
       uint2 y[kCbVecs];
@@ -358,16 +401,15 @@ combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict
 #pragma unroll
       for (int u = 0; u < kCbVecs; ++u) {
         const int c = c0 + 32 * u;
-        float fd[8], fy[8], g[8];
-        unpack8(dv[u], fd);
+        float fy[8], g[8];
         const uint32_t b0 = biased(y[u].x), b1 = biased(y[u].y);
         decode4(b0, fy);
         decode4(b1, fy + 4);
         float part = 0.f;   // over the unit's codes; their one scale multiplies the sum
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          part = fmaf(fd[k], fy[k], part);
-          g[k] = mul_bf16_exact(wj, fd[k]);
+          part = fmaf(fd[u][k], fy[k], part);
+          g[k] = mul_bf16_exact(wj, fd[u][k]);
         }
         if (marks(b0) | marks(b1)) part = __uint_as_float(0x7fc00000u);
         dot = fmaf(sc[u], part, dot);
@@ -393,9 +435,15 @@ extern "C" int moe_ckpt8_pack(const moe_bf16* x, int M, int N, int8_t* q, moe_bf
   if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return MOE_ERR_MISALIGNED;
   const int nv = N / 8;
-  const Tiles tl = make_tiles(M, 4 * scale_blocks(nv), kThreads * kPackUnroll);
   cudaStream_t st = as_stream(stream);
   ProfScope prof("ckpt8_pack", st);
+  if (N % 32 == 0) {
+    const long long total = static_cast<long long>(M) * nv;
+    return launch_pdl(pack_flat_kernel, grid_for(total, kThreads * kPackUnroll, 128), kThreads, 0, st,
+                      1, reinterpret_cast<const uint4*>(x), total, reinterpret_cast<uint2*>(q),
+                      reinterpret_cast<uint16_t*>(s));
+  }
+  const Tiles tl = make_tiles(M, 4 * scale_blocks(nv), kThreads * kPackUnroll);
   return launch_pdl(pack_kernel, grid_for(tl.count, 1, 128), kThreads, 0, st, 1,
                     reinterpret_cast<const uint4*>(x), tl, nv, reinterpret_cast<uint2*>(q),
                     reinterpret_cast<uint16_t*>(s));

@@ -510,7 +510,10 @@ __device__ __forceinline__ void store_cols(float* to, const float (&v)[8]) {
 // The ring: up to 192 KB an SM, four stages of three arrays with 1024 / V threads
 // on it (two stages and 512 threads with four vectors, where d > 8192).
 constexpr int ring_stages(int V) { return V <= 2 ? 4 : 2; }
-constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
+#ifndef NB_T
+#define NB_T 512
+#endif
+constexpr int ring_threads(int V) { return V == 1 ? 1024 : V == 2 ? NB_T : 512; }
 
 // With a = dout (or dxn), b = z (or x) and k = gain (times the gate's row and
 // scale where the gate has d columns, those being constant over a span), a row
@@ -603,6 +606,7 @@ __global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(Backw
     const float w = rs * (kVec ? 1.f : sg);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      if ((lane & ~31) + v * G >= nv) break;   // nothing for this warp
       unpack8(ring[slot(stage, 0, v)], a[v]);
       unpack8(ring[slot(stage, 1, v)], b[v]);
 #pragma unroll
@@ -750,11 +754,14 @@ struct BackwardPlan {
   int V;
 };
 
-BackwardPlan plan_backward(int T, int d) {
+BackwardPlan plan_backward(int T, int d, int arrays) {
   BackwardPlan p;
   p.V = d <= 8 * NB_CUT ? 1 : d <= 8192 ? 2 : 4;
   p.rows = plan_rows(d, p.V);
-  p.chunks = plan_chunks(T, p.rows, std::max(1, ring_threads(p.V) / p.rows.block()));
+  const int smem = 16 * ring_stages(p.V) * arrays * p.V * p.rows.block();
+  const int resident = std::min(ring_threads(p.V) / p.rows.block(),
+                                kSmemPerSm / (smem + kSmemReserved));
+  p.chunks = plan_chunks(T, p.rows, std::max(1, resident));
   return p;
 }
 
@@ -784,7 +791,7 @@ int run_backward(const BackwardPlan& p, const BackwardArgs& a, bool norm, int ga
 
 int launch_backward(const char* name, BackwardArgs a, int T, int d, bool norm, int gate,
                     float* dgain, void* ws, cudaStream_t st) {
-  const BackwardPlan p = plan_backward(T, d);
+  const BackwardPlan p = plan_backward(T, d, a.dres ? 3 : 2);
   float* scratch = reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspaceHeader);
   const size_t slots = static_cast<size_t>(p.chunks.workers) * d;
   a.part_gain = scratch;
@@ -836,7 +843,7 @@ int zero_sums(float* dgain, long long n_gain, float* dgate, long long n_gate, cu
 
 size_t norm_backward_workspace(int T, int d) {
   if (!norm_shape_ok(T, d) || d > kMaxD) return 0;
-  const BackwardPlan p = plan_backward(T, d);
+  const BackwardPlan p = plan_backward(T, d, 2);   // the most groups
   return kWorkspaceHeader + sizeof(float) * (static_cast<size_t>(p.chunks.workers) * d * 3 + T);
 }
 
