@@ -73,6 +73,13 @@ __device__ __forceinline__ void decode4(uint32_t b, float* v) {
     v[i] = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 | i)) - 8388736.f;   // 2^23 + 128
 }
 
+// Codes i and i + 1 of a biased word as a pair of floats (exact).
+__device__ __forceinline__ float_pair decode2(uint32_t b, int i) {
+  const float_pair v = make_pair(__uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 | i)),
+                                 __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7441 | i)));
+  return add_pair(v, make_pair(-8388736.f, -8388736.f));
+}
+
 // Nonzero if a biased word holds a mark (a zero byte).
 __device__ __forceinline__ uint32_t marks(uint32_t b) { return (b - 0x01010101u) & ~b & 0x80808080u; }
 
@@ -401,16 +408,17 @@ combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict
 #pragma unroll
       for (int u = 0; u < kCbVecs; ++u) {
         const int c = c0 + 32 * u;
-        float fy[8], g[8];
+        float g[8];
         const uint32_t b0 = biased(y[u].x), b1 = biased(y[u].y);
-        decode4(b0, fy);
-        decode4(b1, fy + 4);
-        float part = 0.f;   // over the unit's codes; their one scale multiplies the sum
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          part = fmaf(fd[u][k], fy[k], part);
+        float_pair part2 = make_pair(0.f, 0.f);   // over the unit's codes; their one scale
+#pragma unroll                                     // multiplies the sum
+        for (int k = 0; k < 8; k += 2) {
+          part2 = fma_pair(make_pair(fd[u][k], fd[u][k + 1]), decode2(k < 4 ? b0 : b1, k & 3), part2);
           g[k] = mul_bf16_exact(wj, fd[u][k]);
+          g[k + 1] = mul_bf16_exact(wj, fd[u][k + 1]);
         }
+        const float2 both = split_pair(part2);
+        float part = both.x + both.y;
         if (marks(b0) | marks(b1)) part = __uint_as_float(0x7fc00000u);
         dot = fmaf(sc[u], part, dot);
         if (c < nv && row >= 0) stg_v4(dy + row * nv + c, pack8(g));

@@ -133,6 +133,51 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
   return v;
 }
 
+// Pairs of floats in one 64-bit register: sm_100's two-wide fp32 arithmetic does
+// two elements per instruction, each rounded as alone.
+typedef unsigned long long float_pair;
+
+__device__ __forceinline__ float_pair make_pair(float lo, float hi) {
+  float_pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split_pair(float_pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ float_pair mul_pair(float_pair a, float_pair b) {
+  float_pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair add_pair(float_pair a, float_pair b) {
+  float_pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair fma_pair(float_pair a, float_pair b, float_pair c) {
+  float_pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The bf16 pair of a word, and eight bf16 as four pairs.
+__device__ __forceinline__ float_pair bf16_pair(uint32_t v) { return make_pair(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ void unpack8(const uint4& v, float_pair p[4]) {
+  p[0] = bf16_pair(v.x);
+  p[1] = bf16_pair(v.y);
+  p[2] = bf16_pair(v.z);
+  p[3] = bf16_pair(v.w);
+}
+__device__ __forceinline__ uint32_t pack_pair(float_pair p) {
+  const float2 f = split_pair(p);
+  return pack_bf16(f.x, f.y);
+}
+__device__ __forceinline__ uint4 pack8(const float_pair p[4]) {
+  return make_uint4(pack_pair(p[0]), pack_pair(p[1]), pack_pair(p[2]), pack_pair(p[3]));
+}
+
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

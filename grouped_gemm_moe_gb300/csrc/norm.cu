@@ -107,6 +107,21 @@ __device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+__device__ __forceinline__ void store_pairs(float* to, const float_pair (&v)[4]) {
+  ulonglong2* p = reinterpret_cast<ulonglong2*>(to);
+  p[0] = make_ulonglong2(v[0], v[1]);
+  p[1] = make_ulonglong2(v[2], v[3]);
+}
+
+__device__ __forceinline__ void load_pairs(const float* p, float_pair (&f)[4]) {
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p));
+  const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+  f[0] = a.x;
+  f[1] = a.y;
+  f[2] = b.x;
+  f[3] = b.y;
+}
+
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
                "r"(live ? 16 : 0)
@@ -349,10 +364,10 @@ norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
   const bool has = lane < nv;
   const int arrays = K + 1 + (shared_y ? 1 : 0);
   const long long slots = static_cast<long long>(T) * K;
-  float g[8];
+  float_pair g[4];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) g[q] = 1.f;
-  if (gain && has) load8f(gain + lane * 8, g);
+  for (int q = 0; q < 4; ++q) g[q] = make_pair(1.f, 1.f);
+  if (gain && has) load_pairs(gain + lane * 8, g);
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   auto at = [&](int stage, int array) {
     return (stage * arrays + array) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
@@ -387,47 +402,50 @@ norm_out_ring_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
     pos = look_up(t + S * workers);
     const float next_wt = weight(t + workers);
     const int stage = i % S;
-    float z[8];
+    float_pair z[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] = 0.f;
+    for (int q = 0; q < 4; ++q) z[q] = make_pair(0.f, 0.f);
 #pragma unroll 4
     for (int j = 0; j < K; ++j) {
       const float wj = __shfl_sync(0xffffffffu, wt, j);
-      float f[8];
+      const float_pair w2 = make_pair(wj, wj);
+      float_pair f[4];
       unpack8(ring[at(stage, j)], f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] = fmaf(wj, f[q], z[q]);
+      for (int q = 0; q < 4; ++q) z[q] = fma_pair(w2, f[q], z[q]);
     }
     if (shared_y) {
-      float f[8];
+      float_pair f[4];
       unpack8(ring[at(stage, K + 1)], f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] += f[q];
+      for (int q = 0; q < 4; ++q) z[q] = add_pair(z[q], f[q]);
     }
     const long long own = t * nv + lane;
     if (zsum && live && has) stg_v4(zsum + own, pack8(z));
     float r = 1.f;
     if (gain) {
-      float s = 0.f;
+      float_pair s2 = mul_pair(z[0], z[0]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s = fmaf(z[q], z[q], s);
-      r = rsqrtf(group.sum(s, G, i) * inv_d + eps);
+      for (int q = 1; q < 4; ++q) s2 = fma_pair(z[q], z[q], s2);
+      const float2 both = split_pair(s2);
+      r = rsqrtf(group.sum(both.x + both.y, G, i) * inv_d + eps);
       if (rstd && live && lane == 0) rstd[t] = r;
     }
     if (live && has) {
-      float f[8], gt[8], m = scale * r;
+      float m = scale * r;
+      float_pair f[4], gt[4];
       unpack8(ring[at(stage, K)], f);
       const float* grow =
           gate ? gate + static_cast<long long>(static_cast<unsigned>(t) / span) * gate_cols : nullptr;
       if (grow && gate_cols != 1) {
-        load8f(grow + lane * 8, gt);
+        load_pairs(grow + lane * 8, gt);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) z[q] *= gt[q];
+        for (int q = 0; q < 4; ++q) z[q] = mul_pair(z[q], gt[q]);
       } else if (grow) {
         m *= __ldg(grow);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = fmaf(m, z[q] * g[q], f[q]);
+      for (int q = 0; q < 4; ++q) f[q] = fma_pair(make_pair(m, m), mul_pair(z[q], g[q]), f[q]);
       stg_v4(out + own, pack8(f));
     }
     wt = next_wt;
@@ -501,19 +519,10 @@ struct BackwardArgs {
   int nv, G;
 };
 
-__device__ __forceinline__ void store_cols(float* to, const float (&v)[8]) {
-  float4* p = reinterpret_cast<float4*>(to);
-  p[0] = make_float4(v[0], v[1], v[2], v[3]);
-  p[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 // The ring: up to 192 KB an SM, four stages of three arrays with 1024 / V threads
 // on it (two stages and 512 threads with four vectors, where d > 8192).
 constexpr int ring_stages(int V) { return V <= 2 ? 4 : 2; }
-#ifndef NB_T
-#define NB_T 512
-#endif
-constexpr int ring_threads(int V) { return V == 1 ? 1024 : V == 2 ? NB_T : 512; }
+constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
 
 // With a = dout (or dxn), b = z (or x) and k = gain (times the gate's row and
 // scale where the gate has d columns, those being constant over a span), a row
@@ -538,32 +547,39 @@ __global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(Backw
   const int row0 = min(static_cast<long long>(worker) * A.chunk, static_cast<long long>(A.T));
   const int row1 = min(static_cast<long long>(row0) + A.chunk, static_cast<long long>(A.T));
   bool has[V];
-  float k[V][8], dg[V][8], e[V][8];
+  float_pair k[V][4], dg[V][4], e[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     has[v] = lane + v * G < nv;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      k[v][q] = 1.f;
-      dg[v][q] = 0.f;
-      e[v][q] = 0.f;
+    for (int q = 0; q < 4; ++q) {
+      k[v][q] = make_pair(1.f, 1.f);
+      dg[v][q] = make_pair(0.f, 0.f);
+      e[v][q] = make_pair(0.f, 0.f);
     }
-    if (NORM && !kVec && has[v]) load8f(A.gain + (lane + v * G) * 8, k[v]);
+    if (NORM && !kVec && has[v]) load_pairs(A.gain + (lane + v * G) * 8, k[v]);
   }
-  auto slot = [&](int stage, int array, int v) {
-    return ((stage * kArrays + array) * V + v) * nthreads + static_cast<int>(threadIdx.x);
-  };
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  auto issue = [&](int t, int stage) {   // always one group of copies, of nothing past the rows
+  // This thread's slots: array and vector at fixed distances, stages `stage_step` apart.
+  const int vec_step = nthreads, stage_step = kArrays * V * nthreads;
+  const uint4* const mine = ring + threadIdx.x;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16 * threadIdx.x;
+  long long at = static_cast<long long>(min(row0, A.T - 1)) * nv + lane;   // the next row to copy
+  int copied = row0, to = 0;                                               // that row, its stage
+  auto issue = [&]() {   // always one group of copies, of nothing past the rows
+    const bool live = copied < row1;
+    const uint32_t slot = base + 16 * to;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool live = t < row1 && has[v];
-      const long long at = live ? static_cast<long long>(t) * nv + lane + v * G : 0;
-      copy16(base + 16 * slot(stage, 0, v), A.up + at, live);
-      copy16(base + 16 * slot(stage, 1, v), A.x + at, live);
-      if (RES) copy16(base + 16 * slot(stage, 2, v), A.dres + at, live);
+      const bool read = live && has[v];
+      const long long from = has[v] ? at + v * G : at;
+      copy16(slot + 16 * v * vec_step, A.up + from, read);
+      copy16(slot + 16 * (V + v) * vec_step, A.x + from, read);
+      if (RES) copy16(slot + 16 * (2 * V + v) * vec_step, A.dres + from, read);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    ++copied;
+    if (copied < row1) at += nv;
+    to = to + stage_step == kStages * stage_step ? 0 : to + stage_step;
   };
   auto row_scalars = [&](int t, float& r, float& sg) {
     r = 1.f;
@@ -573,101 +589,111 @@ __global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(Backw
       if (GATE == kGateScalar) sg *= __ldg(A.gate + (A.span == 1 ? t : t / A.span));
     }
   };
+  if (lane >= nv) at -= lane;   // a thread without a vector copies nothing, from a place that exists
 #pragma unroll
-  for (int st = 0; st + 1 < kStages; ++st) issue(row0 + st, st);
+  for (int st = 0; st + 1 < kStages; ++st) issue();
   float rs, sg;
   row_scalars(row0, rs, sg);
-  int span_id = 0;
-  long long span_end = -1;
+  int span_id = 0, span_end = -1, stage = 0;
   for (int i = 0; i < A.chunk; ++i) {   // every group of a block runs every step
     const int t = row0 + i;
     const bool live = t < row1;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    issue(t + kStages - 1, (i + kStages - 1) % kStages);   // the slots of row t - 1, read by now
-    const int stage = i % kStages;
+    copies_wait<kStages - 2>();
+    issue();   // into the slots of row t - 1, read by now
+    const uint4* const row = mine + stage;
+    stage = stage + stage_step == kStages * stage_step ? 0 : stage + stage_step;
     if (kVec && live && t >= span_end) {   // a span begins (or is entered)
       span_id = t / A.span;
-      span_end = (span_id + 1LL) * A.span;
+      span_end = static_cast<int>(min((span_id + 1LL) * A.span, static_cast<long long>(A.T)));
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!has[v]) break;
         const int c = (lane + v * G) * 8;
-        float gn[8];
-        load8f(A.gate + span_id * (nv * 8LL) + c, k[v]);
-        if (NORM) load8f(A.gain + c, gn);
+        float_pair gn[4];
+        load_pairs(A.gate + span_id * (nv * 8LL) + c, k[v]);
+        if (NORM) load_pairs(A.gain + c, gn);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) k[v][q] *= NORM ? A.scale * gn[q] : A.scale;
+        for (int q = 0; q < 4; ++q) {
+          k[v][q] = mul_pair(k[v][q], make_pair(A.scale, A.scale));
+          if (NORM) k[v][q] = mul_pair(k[v][q], gn[q]);
+        }
       }
     }
     float nrs, nsg;
     row_scalars(t + 1, nrs, nsg);
-    float a[V][8], b[V][8];
-    float s = 0.f;
+    float_pair a[V][4], b[V][4], s2 = make_pair(0.f, 0.f);
     const float w = rs * (kVec ? 1.f : sg);
+    const float_pair w2 = make_pair(w, w);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if ((lane & ~31) + v * G >= nv) break;   // nothing for this warp
-      unpack8(ring[slot(stage, 0, v)], a[v]);
-      unpack8(ring[slot(stage, 1, v)], b[v]);
+      unpack8(row[v * vec_step], a[v]);
+      unpack8(row[(V + v) * vec_step], b[v]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float p = a[v][q] * b[v][q];
-        if (kVec) e[v][q] = fmaf(p, rs, e[v][q]);
-        else if (NORM) dg[v][q] = fmaf(p, w, dg[v][q]);
-        s = fmaf(p, k[v][q], s);
+      for (int q = 0; q < 4; ++q) {
+        const float_pair p = mul_pair(a[v][q], b[v][q]);
+        if (kVec) e[v][q] = fma_pair(p, w2, e[v][q]);
+        else if (NORM) dg[v][q] = fma_pair(p, w2, dg[v][q]);
+        s2 = fma_pair(p, k[v][q], s2);
       }
     }
-    if (NORM || GATE == kGateScalar) s = group.sum(s, G, i);
+    float s = 0.f;
+    if (NORM || GATE == kGateScalar) {
+      const float2 both = split_pair(s2);
+      s = group.sum(both.x + both.y, G, i);
+    }
     if (GATE == kGateScalar && live && lane == 0) A.row_dot[t] = A.scale * rs * s;
-    const float wa = rs * sg, wb = -(rs * rs) * (s * rs * sg * A.inv_d);
     if (live) {
+      const float wa = rs * sg, wb = -(rs * rs) * (s * rs * sg * A.inv_d);
+      const float_pair wa2 = make_pair(wa, wa), wb2 = make_pair(wb, wb);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!has[v]) break;
-        float o[8];
-        if (RES) unpack8(ring[slot(stage, 2, v)], o);
+        float_pair o[4];
+        if (RES) unpack8(row[(2 * V + v) * vec_step], o);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float d = RES ? o[q] : 0.f;
-          if (NORM) d = RES ? fmaf(wb, b[v][q], d) : wb * b[v][q];
-          o[q] = fmaf(wa, k[v][q] * a[v][q], d);
+        for (int q = 0; q < 4; ++q) {
+          const float_pair ka = mul_pair(k[v][q], a[v][q]);
+          if (NORM) o[q] = RES ? fma_pair(wb2, b[v][q], o[q]) : mul_pair(wb2, b[v][q]);
+          o[q] = (NORM || RES) ? fma_pair(wa2, ka, o[q]) : mul_pair(wa2, ka);
         }
         stg_v4(A.dx + static_cast<long long>(t) * nv + lane + v * G, pack8(o));
       }
     }
     if (kVec && live && (t + 1 == span_end || t + 1 == row1)) {
       const long long begin = static_cast<long long>(span_id) * A.span;
-      const long long end = min(span_end, static_cast<long long>(A.T));
-      float* to = begin < row0 ? A.part_gate0 + worker * (nv * 8LL)
-                  : end > row1 ? A.part_gate1 + worker * (nv * 8LL)
-                               : A.dgate + span_id * (nv * 8LL);
+      float* to_row = begin < row0 ? A.part_gate0 + worker * (nv * 8LL)
+                      : span_end > row1 ? A.part_gate1 + worker * (nv * 8LL)
+                                        : A.dgate + span_id * (nv * 8LL);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!has[v]) break;
         const int c = (lane + v * G) * 8;
-        float gn[8], gt[8], o[8];
+        float_pair gn[4], gt[4], o[4];
         if (NORM) {
-          load8f(A.gain + c, gn);
-          load8f(A.gate + span_id * (nv * 8LL) + c, gt);
+          load_pairs(A.gain + c, gn);
+          load_pairs(A.gate + span_id * (nv * 8LL) + c, gt);
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float se = A.scale * e[v][q];
-          o[q] = NORM ? gn[q] * se : se;
-          if (NORM) dg[v][q] = fmaf(gt[q], se, dg[v][q]);
-          e[v][q] = 0.f;
+        for (int q = 0; q < 4; ++q) {
+          o[q] = mul_pair(make_pair(A.scale, A.scale), e[v][q]);
+          if (NORM) {
+            dg[v][q] = fma_pair(gt[q], o[q], dg[v][q]);
+            o[q] = mul_pair(gn[q], o[q]);
+          }
+          e[v][q] = make_pair(0.f, 0.f);
         }
-        store_cols(to + c, o);
+        store_pairs(to_row + c, o);
       }
     }
     rs = nrs;
     sg = nsg;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  copies_wait<0>();
   if (NORM && row0 < A.T) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (has[v]) store_cols(A.part_gain + worker * (nv * 8LL) + (lane + v * G) * 8, dg[v]);
+      if (has[v]) store_pairs(A.part_gain + worker * (nv * 8LL) + (lane + v * G) * 8, dg[v]);
   }
 }
 
