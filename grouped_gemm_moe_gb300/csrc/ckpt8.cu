@@ -16,11 +16,16 @@
 // within a block of 32 the uniform step of max / 127 leaves about a fifth of
 // E4M3's error on values of one spread (0.5 % against 2.6 % of their RMS).
 //
-// All four kernels stream their arrays once and are bound by HBM. The
-// conversions go through the fp32 significand (add and subtract 1.5 * 2^23, or
-// 2^23 with the code's byte as the low bits), which keeps them on the FMA pipes:
-// the conversion instructions run at an eighth of that rate and would bound the
-// kernels that write more than they read.
+// All kernels stream their arrays once and are bound by HBM, with the logic pipe
+// (which issues every second cycle) next. The conversions go through the fp32
+// significand (add and subtract 1.5 * 2^23, or 2^23 with the code's byte as the
+// low bits), which keeps them on the FMA pipes: the conversion instructions run at
+// an eighth of that rate and would bound the kernels that write more than they read.
+//
+// Measured on one GB300, a call of both directions in turn (HBM floor at 6.8 TB/s):
+//   rows 16384 x 2048 packed, dispatched to 6 experts each    83 us (80)
+//   [G | U] 65536 x 1536 packed, restored with H             113 us (105)
+//   combine gradient, 8191 tokens, K = 8, d = 2048            77 us (65)
 #include <algorithm>
 
 #include "common.cuh"

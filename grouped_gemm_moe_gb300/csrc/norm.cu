@@ -15,16 +15,23 @@
 //
 // Every kernel reads each row once and is bound by HBM. A row group of G
 // threads (whole warps) owns one row at a time, V 16-byte vectors per thread,
-// so a row stays in registers between its sum and its result. The forward
-// kernels take narrow groups (V = 8 or 4: few threads wait for a row's sum, and
-// many rows are in flight) once there are rows to fill the SMs, and one
-// vector per thread before that, where the latency of a row counts. The
-// gradient kernels keep column sums (dg, dgate) in registers over a group's
-// contiguous rows, so they stay at one or two vectors per thread and get their
-// bytes in flight from a ring in shared memory that every thread fills
-// for itself (cp.async; a thread reads only what it copied, so no barrier
-// guards the ring). Groups write their column sums once to the workspace and a
-// second launch adds them in a fixed order: no atomics, the same bits every run.
+// so a row is read once and stays in the SM between its sum and its result. Its
+// bytes come through a ring in shared memory that every thread fills for itself
+// (cp.async; a thread reads only what it copied, so no barrier guards the ring):
+// the rows ahead are in flight while this one waits for its sum, at no registers.
+// Once the ring kept HBM busy, the instructions per row decided: several vectors
+// per thread (fewer threads take part in a row's sum), algebra that shares factors
+// over a row or a span, and two-wide fp32 arithmetic. The gradient kernels keep
+// column sums (dg, dgate) in registers over a group's contiguous rows, write them
+// once to the workspace, and a second launch adds them in a fixed order: no
+// atomics, the same bits every run.
+//
+// Measured on one GB300, device time a call (HBM floor at 6.8 TB/s in brackets):
+//   norm_in           32768 x 4096                        90 us (79); 2.2 us for one row
+//   norm_out          8192 x 2048, K = 8, channel gate    57 us (54); 3.2 us for 16 rows
+//   norm_in_backward  32768 x 4096 with the residual     161 us (158)
+//   norm_out_backward 16383 x 2056, gate per 1000 rows    46 us (30): 4 us of it the join
+//                     and about 4 more the spans' partial sums; 36 us at 2048 without a gate
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,15 +39,6 @@
 namespace moe {
 namespace {
 
-#ifndef NI_CUT1
-#define NI_CUT1 128
-#endif
-#ifndef NI_CUT2
-#define NI_CUT2 256
-#endif
-#ifndef NB_CUT
-#define NB_CUT 32
-#endif
 constexpr int kMaxD = 16384;
 
 // How rows of nv vectors map to threads: G threads per row group (a multiple of
@@ -72,7 +70,6 @@ struct GroupSum {
     slot = first * 4 + lane / 32;
     if (G > 32) {
       if (threadIdx.x < 64) buf[threadIdx.x] = 0.f;
-      if (blockDim.x < 64 && threadIdx.x < 32) buf[32 + threadIdx.x] = 0.f;
       __syncthreads();
     }
   }
@@ -97,8 +94,6 @@ struct GroupSum {
 // thread and 512 from four on.
 constexpr int in_stages(int V) { return V == 1 ? 8 : 4; }
 constexpr int in_threads(int V) { return V <= 2 ? 1024 : 512; }
-
-constexpr int max_threads(int V) { return V == 1 ? 1024 : 256; }
 
 __device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
@@ -240,7 +235,7 @@ norm_in_kernel(const uint4* __restrict__ x, const float* __restrict__ gain, floa
 // the combine of this library, and z is never rounded on its way into the norm;
 // only the copy saved for the gradient is bf16.
 template <int KC, int V>
-__global__ void __launch_bounds__(max_threads(V), V == 1 ? 1 : 2)
+__global__ void __launch_bounds__(256, 2)
 norm_out_kernel(const uint4* __restrict__ y, const float* __restrict__ w,
                 const int32_t* __restrict__ inv_perm, int K, const uint4* __restrict__ shared_y,
                 const uint4* resid, const float* __restrict__ gain,
@@ -490,8 +485,10 @@ int launch_big(void (*kern)(KArgs...), int& configured, int grid, int block, siz
   return launch_pdl(kern, grid, block, smem, st, 1, args...);
 }
 
-// Calls with few rows take a block per row.
-bool few_rows(int T) { return T <= 2 * num_sms(); }
+// norm_in with few rows takes a block per row: 1.9 against 2.1 us for one row of
+// d = 4096, 2.4 against 2.7 for 608 rows of 2048; at 1024 rows of 4096 the ring wins
+// (4.7 against 5.0 us).
+bool few_rows(int T) { return T <= 4 * num_sms(); }
 
 // ----------------------------------------------------------------- gradients
 // A row group takes `chunk` consecutive rows. Its column sums go to slot arrays
@@ -519,8 +516,9 @@ struct BackwardArgs {
   int nv, G;
 };
 
-// The ring: up to 192 KB an SM, four stages of three arrays with 1024 / V threads
-// on it (two stages and 512 threads with four vectors, where d > 8192).
+// The ring: four stages, 128 or (of three arrays) 192 KB an SM with 1024 / V threads
+// on it, two stages and 512 threads with four vectors (d > 8192). Six stages of
+// two arrays measured 3 to 5 % slower than four.
 constexpr int ring_stages(int V) { return V <= 2 ? 4 : 2; }
 constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
 
@@ -697,29 +695,29 @@ __global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(Backw
   }
 }
 
-// Joins the groups' column sums: blockIdx.x picks 32 columns, the warps take the
-// groups in turn, then one fixed tree. blockIdx.y = 0 sums dgain; the others
-// stand for the spans (by_span) or for the groups, whichever are fewer, and sum
-// the span if it crosses groups (of a group: the span that begins in its rows and
-// goes on past them).
-constexpr int kJoinWarps = 16;
-
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// Joins the groups' column sums: blockIdx.x picks 16 columns, the quads of threads
+// (a float4 each) take the groups in turn, eight loads at once, then one fixed
+// tree. Task 0 sums dgain; the others stand for the spans (by_span) or for the
+// groups, whichever are fewer, and sum the span if it crosses groups (of a group:
+// the span that begins in its rows and goes on past them).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
 norm_join_kernel(const float* part_gain, const float* part_gate0, const float* part_gate1, int d,
-                 int workers, int chunk, int T, int span, int by_span, float* dgain,
-                 float* dgate) {
+                 int workers, int chunk, int T, int span, int by_span, int task0,
+                 float* dgain, float* dgate) {
   pdl_enter();
-  __shared__ float acc[kJoinWarps][33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float4 acc[THREADS / 32][4];
+  const int warp = threadIdx.x >> 5, quad = threadIdx.x & 3;
+  const int c = blockIdx.x * 16 + quad * 4;
   const float* first = nullptr;   // a row added to the sum of rows [a, b) of `rest`
   const float* rest = part_gain;
   float* to = dgain;
   int a = 0, b = workers;
-  if (blockIdx.y == 0) {
+  const int task = task0 + blockIdx.y;
+  if (task == 0) {
     if (!dgain) return;
   } else {
-    const long long k = blockIdx.y - 1;
+    const long long k = task - 1;
     const long long s = by_span ? k : min((k + 1) * chunk, static_cast<long long>(T)) - 1;
     const long long id = by_span ? s : s / span;
     const long long begin = id * span, end = min(begin + span, static_cast<long long>(T));
@@ -732,18 +730,29 @@ norm_join_kernel(const float* part_gain, const float* part_gate0, const float* p
     b = static_cast<int>((end - 1) / chunk) + 1;
     to = dgate + id * d;
   }
-  float s = 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float4& x, const float4& y) {
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  };
   if (c < d) {
 #pragma unroll 8
-    for (int w = a + warp; w < b; w += kJoinWarps) s += __ldcg(rest + static_cast<long long>(w) * d + c);
+    for (int w = a + (threadIdx.x >> 2); w < b; w += THREADS / 4)
+      add(s, __ldcg(reinterpret_cast<const float4*>(rest + static_cast<long long>(w) * d + c)));
   }
-  acc[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < d) {
-    float t = first ? __ldcg(first + c) : 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) t += acc[w][lane];
-    to[c] = t;
+  for (int o = 4; o < 32; o <<= 1)
+    add(s, make_float4(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o),
+                       __shfl_xor_sync(0xffffffffu, s.z, o), __shfl_xor_sync(0xffffffffu, s.w, o)));
+  if ((threadIdx.x & 31) < 4) acc[warp][quad] = s;
+  __syncthreads();
+  if (threadIdx.x < 4 && c < d) {
+    float4 t = first ? __ldcg(reinterpret_cast<const float4*>(first + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) add(t, acc[w][quad]);
+    *reinterpret_cast<float4*>(to + c) = t;
   }
 }
 
@@ -782,7 +791,8 @@ struct BackwardPlan {
 
 BackwardPlan plan_backward(int T, int d, int arrays) {
   BackwardPlan p;
-  p.V = d <= 8 * NB_CUT ? 1 : d <= 8192 ? 2 : 4;
+  // 16383 x 2056: 47 us with two vectors a thread, 64 with one (registers spill at 1024 threads)
+  p.V = d <= 256 ? 1 : d <= 8192 ? 2 : 4;
   p.rows = plan_rows(d, p.V);
   const int smem = 16 * ring_stages(p.V) * arrays * p.V * p.rows.block();
   const int resident = std::min(ring_threads(p.V) / p.rows.block(),
@@ -841,10 +851,25 @@ int launch_backward(const char* name, BackwardArgs a, int T, int d, bool norm, i
   if (norm || gate == kGateVector) {
     ProfScope prof("norm_join", st);
     const int spans = gate == kGateVector ? (T - 1) / a.span + 1 : 0;
-    const dim3 grid((d + 31) / 32, 1 + std::min(spans, p.chunks.workers));
-    rc = launch_pdl(norm_join_kernel, grid, kJoinWarps * 32, 0, st, 1, a.part_gain, a.part_gate0,
-                    a.part_gate1, d, p.chunks.workers, p.chunks.chunk, T, a.span,
-                    static_cast<int>(spans <= p.chunks.workers), norm ? dgain : nullptr, a.dgate);
+    const int workers = p.chunks.workers, gates = std::min(spans, workers);
+    // Tasks [task0, task0 + tasks), `rows` groups each at most: 256 threads take 512
+    // of them in one round of loads, and short rows make more groups than that.
+    auto join = [&](int task0, int tasks, int rows) {
+      auto go = [&](auto kern, int threads) {
+        return launch_pdl(kern, dim3((d + 15) / 16, tasks), threads, 0, st, 1, a.part_gain,
+                          a.part_gate0, a.part_gate1, d, workers, p.chunks.chunk, T, a.span,
+                          static_cast<int>(spans <= workers), task0, norm ? dgain : nullptr,
+                          a.dgate);
+      };
+      return rows <= 1024 ? go(norm_join_kernel<256>, 256) : go(norm_join_kernel<1024>, 1024);
+    };
+    const int span_rows = a.span / p.chunks.chunk + 2;
+    if (gates == 0 || (workers <= 1024) == (span_rows <= 1024)) {
+      rc = join(0, 1 + gates, workers);
+    } else {   // many groups, short spans
+      rc = norm ? join(0, 1, workers) : MOE_OK;
+      if (rc == MOE_OK) rc = join(1, gates, span_rows);
+    }
     if (rc != MOE_OK) return rc;
   }
   if (gate == kGateScalar && !direct) {
@@ -906,8 +931,9 @@ extern "C" int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, f
     return launch_big(norm_in_ring_kernel<V>, configured, c.grid, p.block(), smem, st, xi, gain, eps,
                       inv_d, T, c.chunk, nv, p.G, xo, rstd);
   };
-  if (nv <= NI_CUT1) return go(std::integral_constant<int, 1>());
-  if (nv <= NI_CUT2) return go(std::integral_constant<int, 2>());
+  // 32768 x 4096 takes 90 us with four vectors a thread, 95 with two, 94 with one
+  if (nv <= 128) return go(std::integral_constant<int, 1>());
+  if (nv <= 256) return go(std::integral_constant<int, 2>());
   return go(std::integral_constant<int, 4>());
 }
 
@@ -966,7 +992,7 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
   const int arrays = K + 1 + (shared_y ? 1 : 0);
   const int S = arrays <= 4 ? 4 : 2;
   const size_t smem = sizeof(uint4) * S * arrays * wide.block();
-  if (!few_rows(T) && nv <= 1024 && smem <= kSmemPerBlock - 1024) {
+  if (nv <= 1024 && smem <= kSmemPerBlock - 1024) {
     const int resident = std::min<int>(std::max(1, 1024 / wide.block()),
                                        kSmemPerSm / static_cast<int>(smem + kSmemReserved));
     const ChunkPlan c = plan_chunks(T, wide, std::max(1, resident));
@@ -978,7 +1004,7 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
     };
     return S == 2 ? go(norm_out_ring_kernel<2>) : go(norm_out_ring_kernel<4>);
   }
-  const int V = few_rows(T) && nv <= 1024 ? 1 : nv <= 1024 ? 4 : 8;
+  const int V = nv <= 1024 ? 4 : 8;   // many slots or long rows: the gathers stay in registers
   const RowPlan p = plan_rows(d, V);
   const unsigned grid = (static_cast<unsigned>(T) + p.groups - 1) / p.groups;
   auto go = [&](auto kern) {
@@ -992,7 +1018,6 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
     if (K <= 4) return go(norm_out_kernel<4, N>);
     return go(norm_out_kernel<8, N>);
   };
-  if (V == 1) return by_k(std::integral_constant<int, 1>());
   if (V == 4) return by_k(std::integral_constant<int, 4>());
   return by_k(std::integral_constant<int, 8>());
 }

@@ -5,8 +5,9 @@
 //   consecutive elements along K;  H = bf16(silu(X Wg) * (X Wu)),  Y = bf16(H Wd)
 //
 // With a few rows per expert the products are bound by reading the weights
-// (half a byte each, plus 2 / group), so the design is about a steady weight
-// stream and few instructions per weight. Weights are laid out once in the order
+// (half a byte each, plus 2 / group), and next by the instructions that unpack
+// them: the logic pipe issues every second cycle, and at HBM speed an SM has 42
+// cycles for the 2048 weights of a k-tile. Weights are laid out once in the order
 // the tensor cores take them: tiles of 32 outputs x 64 K, 1 KB, twice 16 bytes per
 // lane, which feed eight m16n8k16 products whose A is the weights and whose 8
 // columns are rows of X. A code becomes the bf16 integer 128 + q in registers
@@ -17,10 +18,15 @@
 //
 // mma.sync and not tcgen05: the A operand is made in registers from 4-bit codes
 // and N is 8 to 32; tcgen05 would take it through shared memory or TMEM at
-// M = 128 for a product that is bound by HBM either way.
+// M = 128 for a product that is bound by HBM and by the unpacking either way.
 //
 // Gate and up share tiles: of each 16 outputs the first eight are gate columns,
 // the others the same up columns, which puts G and U of one element in one lane.
+//
+// Measured on one GB300, both products, device time a call (floor: the weights of
+// the experts that have rows at 6.8 TB/s): 128 experts, K 8, d 2048, I 768, group
+// 128: 1 token 12 us (2.9), 16 tokens 48 us (30), 64 tokens 65 us (46); 64 experts,
+// K 6, d 2048, I 1408, group 64: 16 tokens 50 us (34).
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,24 +34,6 @@
 namespace moe {
 namespace {
 
-#ifndef W4_WANT
-#define W4_WANT 72
-#endif
-#ifndef W4_BLK
-#define W4_BLK 3
-#endif
-#ifndef W4_MIN
-#define W4_MIN 20000
-#endif
-#ifndef W4_CUT0
-#define W4_CUT0 8
-#endif
-#ifndef W4_CUT1
-#define W4_CUT1 6
-#endif
-#ifndef W4_CUT2
-#define W4_CUT2 12
-#endif
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
@@ -457,7 +445,7 @@ __device__ __forceinline__ void pass(const W4Args& A, int e, int it, int ks, int
 
 // NTMAX: the most groups of 8 rows a pass takes (a power of two).
 template <bool GATE_UP, int S, int NTMAX, int GROUP>
-__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? W4_BLK : 2) w4_kernel(W4Args A) {
+__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 3 : 2) w4_kernel(W4Args A) {
   pdl_enter();
   extern __shared__ uint4 ring[];   // [warp][stage][codes, scales]
   const int e = expert_of(A.offsets, A.E, blockIdx.y, gridDim.y == static_cast<unsigned>(A.E));
@@ -768,15 +756,28 @@ int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
   return launch_pdl(kern, num_sms(), kDThreads, smem, st, 1, a, cap);
 }
 
+// The persistent kernel is for few rows per expert (mean, rounded up) and enough
+// k-tiles to share; its measured times against the other kernel's, both products:
+//   1 row  (16 tokens, 128 experts, K 8, d 2048, I 768)   48 : 58 us
+//   4 rows (64 tokens)                                    65 : 83 us
+//   8 rows (128 tokens)                                   87 : 97 us
+//   12 rows (128 tokens, 64 experts, K 6, I 1408)        109 : 107 us
+// and by the k-tiles of the gate and up products, at most 1 row:
+//   33 K (1 token, 32 experts, K 4, d 4096, I 2048)       21 : 22 us
+//   12 K (1 token, 128 experts, K 8, d 2048, I 768)       15 : 12 us
+constexpr int kDecodeRows = 8;
+constexpr int kDecodeTiles = 20000;
+
 // most_rows: a bound on the rows of one expert.
 template <bool GATE_UP>
 int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st) {
   const int slots = std::min(a.E, a.M);
-  const int mean_rows = static_cast<int>(std::min<long long>(most_rows, (static_cast<long long>(a.M) + a.E - 1) / a.E));
+  const int mean_rows = std::min(most_rows, (a.M - 1) / a.E + 1);
   const long long entries = a.E + a.M / 8;   // at most
   const int cap = decode_rows(a.group, a.K, a.E);
   const long long k_tiles = static_cast<long long>(slots) * a.nt * (a.K / 64);
-  if (mean_rows <= W4_CUT0 && k_tiles >= W4_MIN && cap >= 8 && entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
+  if (mean_rows <= kDecodeRows && k_tiles >= kDecodeTiles && cap >= 8 &&
+      entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
     ProfScope prof(name, st);
     if (a.group == 32) return launch_decode<GATE_UP, 32>(a, cap, st);
     if (a.group == 64) return launch_decode<GATE_UP, 64>(a, cap, st);
@@ -784,7 +785,7 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
   }
   // Split K until the launch has about 24 warps per SM three times over, a warp
   // keeping four k-tiles at least.
-  const long long want = static_cast<long long>(num_sms()) * W4_WANT;
+  const long long want = static_cast<long long>(num_sms()) * 72;
   const long long tiles = static_cast<long long>(slots) * a.nt;
   int S = 1;
   while (S < 8 && tiles * S < want && a.K / 64 >= 8 * S) S *= 2;
@@ -796,8 +797,12 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
     if (a.group == 64) return launch_split<GATE_UP, N, 64>(S, grid, a, st);
     return launch_split<GATE_UP, N, 128>(S, grid, a, st);
   };
-  if (mean_rows <= W4_CUT1) return by_group(std::integral_constant<int, 1>());
-  if (mean_rows <= W4_CUT2) return by_group(std::integral_constant<int, 2>());
+  // Rows of a pass: the weights are read again for every 8, 16 or 32 rows of an
+  // expert, and the wider passes leave room for fewer warps. 64 tokens at 128
+  // experts (4 rows) 83, 86 and 86 us with 8, 16 and 32 rows a pass; 256 tokens (16
+  // rows) 147 us with 32, where 8 rows a pass would read the weights twice.
+  if (mean_rows <= 6) return by_group(std::integral_constant<int, 1>());
+  if (mean_rows <= 12) return by_group(std::integral_constant<int, 2>());
   return by_group(std::integral_constant<int, 4>());
 }
 
