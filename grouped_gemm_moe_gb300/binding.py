@@ -715,7 +715,7 @@ def moe_grouped_ffn_fp8(xp: torch.Tensor, offsets: torch.Tensor, wgu, wd, save_g
 def _shaped(t: Optional[torch.Tensor], dtype, shape, name: str, dev):
     """_need for a tensor (or None) of a known shape on a known device."""
     if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                     and t.device == dev and t.is_contiguous()):
+                     and t.is_contiguous() and t.device == dev):
         return
     _need(t, dtype, len(shape), name)
     if tuple(t.shape) != tuple(shape):
@@ -800,11 +800,11 @@ def moe_norm_out(y: torch.Tensor, resid: torch.Tensor, gain: Optional[torch.Tens
     _need(y, torch.bfloat16, 2, "y")
     _need(resid, torch.bfloat16, 2, "resid")
     T, d = resid.shape
-    dev = y.device
-    if y.shape[1] != d or (y.shape[0] % T if T else y.shape[0]):
-        raise ValueError(f"y must be [T*K, {d}] with T = {T}, got {tuple(y.shape)}")
-    K = y.shape[0] // T if T else 1
-    _shaped(resid, torch.bfloat16, (T, d), "resid", dev)
+    rows, dy = y.shape
+    dev = resid.device
+    if dy != d or (rows % T if T else rows) or y.device != dev:
+        raise ValueError(f"y must be [T*K, {d}] with T = {T} on {dev}, got {(rows, dy)} on {y.device}")
+    K = rows // T if T else 1
     _shaped(gain, torch.float32, (d,), "gain", dev)
     _shaped(topk_w, torch.float32, (T, K), "topk_w", dev)
     _shaped(inv_perm, torch.int32, (T * K,), "inv_perm", dev)

@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 3 : 2) w4_kernel(W4Args
 // more to do than another, from one token (an item over six warps) to a full batch
 // (five items a warp). An item that crosses warps is finished by the warp that has
 // its first k-tile, from the other warps' sums in shared memory.
+
 constexpr int kDWarps = 16;
 constexpr int kDThreads = kDWarps * 32;
 constexpr int kDRows = 32;                      // most rows of X in shared memory

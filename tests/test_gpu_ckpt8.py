@@ -125,6 +125,23 @@ def test_combine_backward(T, d, k):
                                                   to_dev(inv, I32))[0])
 
 
+@pytest.mark.parametrize("N", [8192, 8208])
+def test_past_two_to_the_31_elements(N):
+    """Rows whose offsets pass 32 bits: the last rows as in a call of their own."""
+    M = 262400
+    x = torch.zeros(M, N, dtype=BF, device=dev())
+    tail = torch.randn(40, N, device=dev()).to(BF)
+    x[-40:] = tail
+    q, s = B.moe_ckpt8_pack(x)
+    qt, st = B.moe_ckpt8_pack(tail)
+    assert torch.equal(q[-40:], qt) and torch.equal(s[-40:], st)
+    assert not q[:-40].any()
+    back = B.moe_ckpt8_dispatch(q, s, out=x)
+    assert torch.equal(back[-40:], B.moe_ckpt8_dispatch(qt, st))
+    _, h = B.moe_ckpt8_swiglu(q, s, out=(x, torch.empty(M, N // 2, dtype=BF, device=dev())))
+    assert torch.equal(h[-40:], B.moe_ckpt8_swiglu(qt, st)[1])
+
+
 def test_a_mark_reaches_the_gradients():
     T, d, k = 4, 64, 2
     rng = np.random.default_rng(8)

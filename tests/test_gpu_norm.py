@@ -220,6 +220,27 @@ def test_zero_rows_and_zero_input():
     assert (xn == 0).all() and torch.allclose(r, torch.full_like(r, 1e3))
 
 
+def test_past_two_to_the_31_elements():
+    """Rows whose offsets pass 32 bits: the last rows as in a call of their own."""
+    T, d = 262400, 8192
+    x = torch.zeros(T, d, dtype=BF, device=dev())
+    tail = torch.randn(64, d, device=dev()).to(BF)
+    x[-64:] = tail
+    gain = torch.rand(d, device=dev()) + 0.5
+    xn, r = B.moe_norm_in(x, gain)
+    want, rw = B.moe_norm_in(tail, gain)
+    assert_bf16_close(f64(xn[-64:]), f64(want), "xn")    # another number of vectors per thread
+    assert torch.allclose(r[-64:], rw, rtol=(d + 16) * U, atol=0)
+    out, z, _ = B.moe_norm_out(xn, x, gain)
+    ow, zw, _ = B.moe_norm_out(xn[-64:].clone(), tail, gain)
+    assert torch.equal(out[-64:], ow) and torch.equal(z[-64:], zw)
+    del out, z
+    dx, dgain = B.moe_norm_in_backward(xn, x, gain, r, x)
+    dw, gw = B.moe_norm_in_backward(xn[-64:].clone(), tail, gain, r[-64:].clone(), tail)
+    assert torch.equal(dx[-64:], dw)
+    assert_sum_close(dgain, f64(xn[-64:]) * f64(tail) * f64(r[-64:])[:, None], 0, "dgain")
+
+
 def test_on_another_stream():
     rng = _rng(13)
     x, gain = to_dev(_bf(rng, 5000, 2048), BF), to_dev(_f32(rng, 2048), F32)

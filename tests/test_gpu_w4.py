@@ -77,6 +77,12 @@ def test_quantize(E, Kd, N, group):
     (3, 512, 256, 128, 32, [65, 0, 100]),
     (40, 128, 128, 32, 64, [0] * 17 + [2] + [0] * 15 + [1] + [0] * 6),   # slots past a ballot
     (2, 4096, 128, 128, 128, [5, 12]),
+    # the persistent kernel: rows past a pass of 8, empty experts between, uneven k-tiles
+    (16, 1024, 704, 64, 64, [1, 0, 9, 8, 0, 3, 17, 0, 0, 2, 8, 1, 7, 0, 0, 16]),
+    (96, 512, 192, 32, 64, [i * 7 % 11 for i in range(96)]),
+    (24, 2048, 768, 128, 32, [8] * 24),
+    (300, 1152, 128, 64, 32, [i % 3 for i in range(300)]),
+    (12, 4096, 1024, 128, 128, [5, 0, 7, 8, 1, 1, 9, 0, 2, 3, 4, 6]),
 ])
 def test_ffn(E, d, I, g_gu, g_d, counts):
     vals, wgu, wd = _experts([E, d, I], E, d, I, g_gu, g_d)
@@ -121,6 +127,32 @@ def test_quantized_bf16_weights_end_to_end():
     wd = B.moe_w4_pack_weights(*plain[2])
     vals = [K.w4_values(*K.w4_quantize(m, 32)) for m in w]
     _check(O.round_bf16(rng.normal(size=(24, d))), np.array([0, 10, 24]), vals, wgu, wd)
+
+
+def test_weights_past_two_to_the_31_bytes():
+    """The last of many experts, whose weights lie past 4 GB."""
+    E, d, I, g = 272, 4096, 4096, 128
+    dv = dev()
+    codes = [torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, device=dv)
+             for n, k in ((I, d), (I, d), (d, I))]
+    scales = [((torch.rand(E, n, k // g, device=dv) + 0.2) * 0.004).to(BF)
+              for n, k in ((I, d), (I, d), (d, I))]
+    wgu = B.moe_w4_pack_weights(codes[0], scales[0], codes[1], scales[1])
+    wd = B.moe_w4_pack_weights(codes[2], scales[2])
+    assert wgu[0].numel() > 1 << 32 and wd[0].numel() > 1 << 31
+    x = O.round_bf16(np.random.default_rng(7).normal(size=(5, d)))
+    counts = np.zeros(E, dtype=np.int64)
+    counts[0], counts[-1] = 2, 3
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    y, h = B.moe_grouped_ffn_w4(to_dev(x, BF), to_dev(offsets, I32), wgu, wd)
+    vals = []
+    for c, s in zip(codes, scales):
+        c = i64(c[[0, -1]])
+        q = np.stack([c & 15, c >> 4], -1).reshape(2, c.shape[1], -1)
+        vals.append(K.w4_values(q, f64(s[[0, -1]])))
+    ry, rh = K.grouped_ffn_w4(x, np.array([0, 2, 5]), *vals, h=f64(h))
+    assert_bf16_close(f64(h), rh, "h")
+    assert_bf16_close(f64(y), ry, "y")
 
 
 def test_not_finite_rows_stay_apart():
