@@ -65,7 +65,7 @@ def parse():
     ap.add_argument("--cpu-sample-tokens", type=int, default=0)
     ap.add_argument("--profile-case", choices=["gemm", "gemm_ragged", "gemm_l2", "gemm_drafter",
                                                "gemm_drafter64", "layer", "hbm", "routing",
-                                               "combine_side", "fp8"],
+                                               "combine_side", "fp8", "block"],
                     default=None,
                     help="run a small fixed case twice for an ncu capture and exit")
     return ap.parse_args()
@@ -95,6 +95,9 @@ def profile_case(which: str):
              full size (T=8192, d=2048, K=8; the routing of the qwen3 inputs), on synthetic
              expert outputs and gradients (~1.1 GB on the device), run twice, with 256 MiB
              of L2-flushing writes before each kernel.
+    block:   the operators around the layer (the norms and their gradients, 8-bit checkpoints,
+             4-bit experts) on each case that perf/operators.py lists, run twice; under 3 GB
+             on the device at a time.
     hbm:     HBM bandwidth by access pattern on 2 GiB fp32 buffers (torch's fill, sum and
              copy; CUDA events, 20 launches after 3 warm-ups): the ceilings that write-only,
              read-only and copy-like kernels are compared with.
@@ -131,6 +134,21 @@ def profile_case(which: str):
     if not os.path.exists(B.LIB_PATH):
         build_mod.build()
     dev = torch.device("cuda:0")
+    if which == "block":
+        from perf import operators
+        operators.own = True
+        for case in operators.listed():
+            state = operators.prepare(case, 1)
+            operators.run(state)
+            torch.cuda.synchronize()
+            B.moe_profile_start(64)
+            operators.run(state)
+            torch.cuda.synchronize()
+            launches = [(name, round(ms * 1e3, 2)) for name, ms in B.moe_profile_stop()]
+            print(json.dumps({"case": case["name"], "us": launches}))
+            del state
+            torch.cuda.empty_cache()
+        return
     g = torch.Generator(device=dev).manual_seed(0)
     flops = {}
     if which in ("gemm", "gemm_ragged", "gemm_l2", "gemm_drafter", "gemm_drafter64"):
