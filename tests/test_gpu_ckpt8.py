@@ -154,6 +154,23 @@ def test_a_mark_reaches_the_gradients():
     assert np.array_equal(np.isnan(f64(dw)).reshape(-1), inv == 3)
 
 
+def test_gradients_that_are_not_finite():
+    """Infinities and NaN of dout go into their own elements of dy, and into their token's dw."""
+    T, d, k = 6, 72, 3
+    rng = np.random.default_rng(9)
+    dout, w, inv = O.round_bf16(rng.normal(size=(T, d))), rng.random((T, k)) + 0.1, rng.permutation(T * k)
+    dout[1, 4], dout[1, 9], dout[4, 70] = np.inf, -np.inf, np.nan
+    q, s = B.moe_ckpt8_pack(to_dev(O.round_bf16(rng.normal(size=(T * k, d))), BF))
+    dy, dw = B.moe_ckpt8_combine_backward(to_dev(dout, BF), q, s, to_dev(w, F32), to_dev(inv, I32))
+    got = f64(dy)[inv.reshape(T, k)]
+    want = w.astype(np.float32).astype(np.float64)[:, :, None] * dout[:, None, :]
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(np.isinf(got), np.isinf(want))
+    assert np.array_equal(np.sign(got[np.isinf(got)]), np.sign(want[np.isinf(want)]))
+    rows = np.isfinite(dout).all(1)
+    assert np.array_equal(np.isfinite(f64(dw)).all(1), rows)
+
+
 def test_no_rows():
     none = torch.empty(0, 64, dtype=BF, device=dev())
     q, s = B.moe_ckpt8_pack(none)
