@@ -27,9 +27,9 @@
 // atomics, the same bits every run.
 //
 // Measured on one GB300, device time a call (HBM floor at 6.8 TB/s in brackets):
-//   norm_in           32768 x 4096                        90 us (79); 2.2 us for one row
+//   norm_in           32768 x 4096                        82 us (79); 2.0 us for one row
 //   norm_out          8192 x 2048, K = 8, channel gate    57 us (54); 3.2 us for 16 rows
-//   norm_in_backward  32768 x 4096 with the residual     161 us (158)
+//   norm_in_backward  32768 x 4096 with the residual     156 us (158)
 //   norm_out_backward 16383 x 2056, gate per 1000 rows    46 us (30): 4 us of it the join
 //                     and about 4 more the spans' partial sums; 36 us at 2048 without a gate
 #include <algorithm>
@@ -90,10 +90,11 @@ struct GroupSum {
   }
 };
 
-// norm_in's ring: 128 KB an SM, with 1024 threads on it up to two vectors a
-// thread and 512 from four on.
-constexpr int in_stages(int V) { return V == 1 ? 8 : 4; }
-constexpr int in_threads(int V) { return V <= 2 ? 1024 : 512; }
+// norm_in's ring: 1024 vectors an SM a stage, 48 KB in flight. More in flight is
+// slower: 32768 x 4096 takes 82 us so, 88 us with a stage more, 90 us with twice the
+// threads (more rows open at once cost HBM more than they hide); less is slower too.
+constexpr int kInStages = 4;
+constexpr int in_threads(int V) { return 1024 / V; }
 
 __device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
@@ -132,12 +133,12 @@ __device__ __forceinline__ void copies_wait() {   // all but the N newest groups
 // stretch of memory), kStages - 1 rows on their way in shared memory. Each thread reads only the vectors it copied itself, so
 // the ring has no barrier of its own.
 template <int V>
-__global__ void __launch_bounds__(in_threads(V), 1)
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
 norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain, float eps,
                     float inv_d, int T, int chunk, int nv, int G, uint4* __restrict__ xn,
                     float* __restrict__ rstd) {
   pdl_enter();
-  constexpr int kStages = in_stages(V);
+  constexpr int kStages = kInStages;
   extern __shared__ uint4 ring[];   // [stage][v][thread]
   __shared__ __align__(16) float red[64];
   const int grp = threadIdx.x / G, lane = threadIdx.x - grp * G;
@@ -516,10 +517,10 @@ struct BackwardArgs {
   int nv, G;
 };
 
-// The ring: four stages, 128 or (of three arrays) 192 KB an SM with 1024 / V threads
-// on it, two stages and 512 threads with four vectors (d > 8192). Six stages of
-// two arrays measured 3 to 5 % slower than four.
-constexpr int ring_stages(int V) { return V <= 2 ? 4 : 2; }
+// The ring: three stages of two or three arrays with 1024 / V threads an SM, two
+// stages and 512 threads with four vectors (d > 8192). 32768 x 4096 with the residual
+// takes 156 us so, 161 with four stages, 164 with two.
+constexpr int ring_stages(int V) { return V <= 2 ? 3 : 2; }
 constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
 
 // With a = dout (or dxn), b = z (or x) and k = gain (times the gate's row and
@@ -926,14 +927,16 @@ extern "C" int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, f
     constexpr int V = decltype(v)::value;
     static thread_local int configured = -1;
     const RowPlan p = plan_rows(d, V);
-    const ChunkPlan c = plan_chunks(T, p, std::max(1, in_threads(V) / p.block()));
-    const size_t smem = sizeof(uint4) * in_stages(V) * V * p.block();
+    const ChunkPlan c = plan_chunks(T, p, (in_threads(V) + p.block() - 1) / p.block());
+    const size_t smem = sizeof(uint4) * kInStages * V * p.block();
     return launch_big(norm_in_ring_kernel<V>, configured, c.grid, p.block(), smem, st, xi, gain, eps,
                       inv_d, T, c.chunk, nv, p.G, xo, rstd);
   };
-  // 32768 x 4096 takes 90 us with four vectors a thread, 95 with two, 94 with one
-  if (nv <= 128) return go(std::integral_constant<int, 1>());
-  if (nv <= 256) return go(std::integral_constant<int, 2>());
+  // One warp a row up to d = 1024 (776 columns take 86 us a GB so, 100 us with one
+  // vector a thread), then as few threads a row as registers allow (2048: 82 us with
+  // four vectors, 86 us with two).
+  if (nv <= 32) return go(std::integral_constant<int, 1>());
+  if (nv <= 64) return go(std::integral_constant<int, 2>());
   return go(std::integral_constant<int, 4>());
 }
 
