@@ -994,12 +994,13 @@ def _w4_weight(w, E: int, per: int, name: str, dev):
     """(outputs of one matrix, K, group) of laid-out weights with `per` of its outputs a tile."""
     tiles, scales = w
     _need(tiles, torch.uint8, 4, name + " tiles")
-    nt, kt = tiles.shape[1], tiles.shape[2]
-    ng = scales.shape[2] if scales.dim() == 4 else 0
-    if tiles.shape[0] != E or tiles.shape[3] != 1024 or ng < 1 or (64 * kt) % ng:
+    _need(scales, torch.bfloat16, 4, name + " scales")
+    e, nt, kt, tile = tiles.shape
+    es, ns, ng, rows = scales.shape
+    if (e, tile, es, ns, rows) != (E, 1024, E, nt, 32) or ng < 1 or (64 * kt) % ng:
         raise ValueError(f"{name} must come from moe_w4_pack_weights for {E} experts")
-    _shaped(tiles, torch.uint8, tuple(tiles.shape), name + " tiles", dev)
-    _shaped(scales, torch.bfloat16, (E, nt, ng, 32), name + " scales", dev)
+    if tiles.device != dev or scales.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
     return nt * per, 64 * kt, 64 * kt // ng
 
 

@@ -610,8 +610,8 @@ int moe_ckpt8_combine_backward(const moe_bf16* dout, const int8_t* q, const moe_
 
 /* ------------------------------------------------------------------------
  * Experts on 4-bit weights with group scales, for the few rows per expert of a
- * decoding batch (any number of rows is accepted; from about 32 rows per expert
- * on, the bf16 and MXFP8 experts are the faster calls):
+ * decoding batch (any number of rows is accepted; from about 22 rows per expert
+ * on the MXFP8 experts are faster, from about 30 the bf16 experts):
  *   w[n][k] = s[n][k / group] (code[n][k] - 8),  codes 0 .. 15, group 32, 64 or 128.
  * A plain 4-bit checkpoint has K contiguous: codes [E, N, K/2] uint8 (element k in
  * the low half of byte k / 2 for even k, in the high half for odd k) and scales
