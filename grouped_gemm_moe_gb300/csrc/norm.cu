@@ -40,6 +40,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxD = 16384;
+constexpr int kMaxGradRows = 1 << 30;   // a gradient's row numbers stay in an int, past its last row too
 
 // How rows of nv vectors map to threads: G threads per row group (a multiple of
 // 32), `groups` groups per block.
@@ -130,8 +131,8 @@ __device__ __forceinline__ void copies_wait() {   // all but the N newest groups
 }
 
 // xn = bf16(x r g) over every workers-th row (the SMs read and write one moving
-// stretch of memory), kStages - 1 rows on their way in shared memory. Each thread reads only the vectors it copied itself, so
-// the ring has no barrier of its own.
+// stretch of memory), kStages - 1 rows on their way in shared memory. Each thread
+// reads only the vectors it copied itself, so the ring has no barrier of its own.
 template <int V>
 __global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
 norm_in_ring_kernel(const uint4* __restrict__ x, const float* __restrict__ gain, float eps,
@@ -894,7 +895,7 @@ int zero_sums(float* dgain, long long n_gain, float* dgate, long long n_gate, cu
 }  // namespace
 
 size_t norm_backward_workspace(int T, int d) {
-  if (!norm_shape_ok(T, d) || d > kMaxD) return 0;
+  if (!norm_shape_ok(T, d) || d > kMaxD || T > kMaxGradRows) return 0;
   const BackwardPlan p = plan_backward(T, d, 2);   // the most groups
   return kWorkspaceHeader + sizeof(float) * (static_cast<size_t>(p.chunks.workers) * d * 3 + T);
 }
@@ -946,7 +947,7 @@ extern "C" int moe_norm_in_backward(const moe_bf16* dxn, const moe_bf16* x, cons
                                     void* stream) {
   using namespace moe;
   if (!norm_shape_ok(T, d)) return MOE_ERR_INVALID_ARG;
-  if (d > kMaxD) return MOE_ERR_UNSUPPORTED;
+  if (d > kMaxD || T > kMaxGradRows) return MOE_ERR_UNSUPPORTED;
   if (!dgain) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dgain)) return MOE_ERR_MISALIGNED;
   cudaStream_t st = as_stream(stream);
@@ -1032,7 +1033,7 @@ extern "C" int moe_norm_out_backward(const moe_bf16* dout, const moe_bf16* zsum,
   using namespace moe;
   if (!norm_shape_ok(T, d)) return MOE_ERR_INVALID_ARG;
   if (gate && (span < 1 || (gate_cols != 1 && gate_cols != d))) return MOE_ERR_INVALID_ARG;
-  if (d > kMaxD) return MOE_ERR_UNSUPPORTED;
+  if (d > kMaxD || T > kMaxGradRows) return MOE_ERR_UNSUPPORTED;
   if ((gain && !dgain) || (gate && !dgate)) return MOE_ERR_INVALID_ARG;
   const void* ptrs[] = {dout, zsum, rstd, gain, gate, dz, dgain, dgate, ws};
   for (const void* p : ptrs)

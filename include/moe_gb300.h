@@ -537,7 +537,7 @@ int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, float eps, m
  *   dx = bf16(dres + r (u - xh mean_c(u xh))),  dgain = sum_t dxn xh.
  *   dxn, x [T,d] bf16, gain [d], rstd [T] in; dres [T,d] bf16 or NULL (zero).
  *   dx [T,d] bf16 out; dgain [d] fp32 out (written, zero when T == 0).
- *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. */
+ *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. T <= 2^30. */
 int moe_norm_in_backward(const moe_bf16* dxn, const moe_bf16* x, const float* gain,
                          const float* rstd, const moe_bf16* dres, int T, int d, moe_bf16* dx,
                          float* dgain, void* ws, size_t ws_bytes, void* stream);
@@ -570,7 +570,7 @@ int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_t* inv_perm
  *   dout, zsum [T,d] bf16, rstd [T] (with a gain), gain, gate as in moe_norm_out.
  *   dz [T,d] bf16 out; dgain [d] fp32 out (with a gain; zero when T == 0); dgate
  *   [ceil(T / span), gate_cols] fp32 out (with a gate).
- *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. */
+ *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. T <= 2^30. */
 int moe_norm_out_backward(const moe_bf16* dout, const moe_bf16* zsum, const float* rstd,
                           const float* gain, const float* gate, int span, int gate_cols,
                           float scale, int T, int d, moe_bf16* dz, float* dgain, float* dgate,

@@ -58,6 +58,16 @@ def test_norm_out(lib):
     assert g(OK, OK, OK, OK, None, 1, 1, 1.0, 4, 16, OK, OK, None, OK, 0, None) == WS
 
 
+def test_norm_gradients_end_at_two_to_the_30_rows(lib):
+    T = (1 << 30) + 1
+    n = 1 << 60
+    assert lib.moe_norm_in_backward(OK, OK, OK, OK, None, T, 8, OK, OK, OK, n, None) == UNSUP
+    assert lib.moe_norm_out_backward(OK, OK, OK, OK, None, 1, 1, 1.0, T, 8, OK, OK, None, OK, n,
+                                     None) == UNSUP
+    assert B.workspace_size(B.MOE_OP_NORM_BACKWARD, T, 1, 1, 1, 8) == 0
+    assert B.workspace_size(B.MOE_OP_NORM_BACKWARD, T - 1, 1, 1, 1, 8) > 0
+
+
 def test_ckpt8(lib):
     assert lib.moe_ckpt8_pack(OK, 4, 12, OK, OK, None) == BAD
     assert lib.moe_ckpt8_pack(OK, 4, 0, OK, OK, None) == BAD
