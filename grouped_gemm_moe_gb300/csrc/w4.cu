@@ -10,9 +10,9 @@
 // cycles for the 2048 weights of a k-tile. Weights are laid out once in the order
 // the tensor cores take them: tiles of 32 outputs x 64 K, 1 KB, twice 16 bytes per
 // lane, which feed eight m16n8k16 products whose A is the weights and whose 8
-// columns are rows of X. A code becomes the bf16 integer 128 + q in registers
-// (exact, two instructions a pair), so the products run on integers and the
-// scale multiplies the fp32 sums of a group: no weight is ever rounded. The
+// columns are rows of X. A code becomes the bf16 integer q - 8 in registers (exact:
+// two logic instructions and a subtraction a pair), so the products run on integers
+// and the scale multiplies the fp32 sums of a group: no weight is ever rounded. The
 // lane's 16 elements of K are two runs of 8, one in each half of the 64, which is
 // the order the rows of X are loaded in 16-byte pieces and keeps groups of 32 apart.
 //
@@ -140,7 +140,9 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t w, int n) {
   return v;
 }
 
-// The same less 136, exactly q - 8.
+// The same less 136, exactly q - 8. The subtraction could be left to the fp32 sums
+// (start them from -136 sum x): that saves up to 2 % (4 % with groups of 32), but
+// the sums would then lose what 136 sum|x| exceeds the result by.
 __device__ __forceinline__ uint32_t centred(uint32_t v) {
   const __nv_bfloat162 c = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), c);
@@ -193,26 +195,6 @@ __device__ __forceinline__ void half_tile(uint32_t w00, uint32_t w01, uint32_t w
       mma16816(p, a1, x[n].z, x[n].w);
       add_scaled(acc[m][n], s[m][0], s[m][1], p);
     }
-  }
-}
-
-// The same against 8 rows without the subtractions: the codes stay 128 + q, and
-// the sums start from less = -136 sum x of the half for the lane's two rows (fp32;
-// what the cancellation leaves is an error of about 2^-19 of the result).
-__device__ __forceinline__ void half_tile_less(uint32_t w00, uint32_t w01, uint32_t w10,
-                                               uint32_t w11, const uint4& x, float2 less, uint2 sc,
-                                               float (&acc)[2][4]) {
-  const float s[2][2] = {{bf16_lo(sc.x), bf16_hi(sc.x)}, {bf16_lo(sc.y), bf16_hi(sc.y)}};
-  const float start[4] = {less.x, less.y, less.x, less.y};
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const uint32_t w0 = m ? w10 : w00, w1 = m ? w11 : w01;
-    const uint32_t a0[4] = {pair_of(w0, 0), pair_of(w1, 0), pair_of(w0, 1), pair_of(w1, 1)};
-    const uint32_t a1[4] = {pair_of(w0, 2), pair_of(w1, 2), pair_of(w0, 3), pair_of(w1, 3)};
-    float p[4];
-    mma16816_from(p, start, a0, x.x, x.y);
-    mma16816(p, a1, x.z, x.w);
-    add_scaled(acc[m], s[m][0], s[m][1], p);
   }
 }
 
@@ -483,18 +465,16 @@ constexpr int row_vecs(int K) { return K / 8 + 4; }   // rows 64 bytes apart mod
 constexpr size_t decode_ring_bytes(int group) {
   return sizeof(uint4) * kDWarps * kStages * stage_vecs(group);
 }
-constexpr size_t decode_row_bytes(int K) {   // a row of X and its sums over 32 K
-  return sizeof(uint4) * row_vecs(K) + sizeof(float) * (K / 32);
-}
+constexpr size_t decode_row_bytes(int K) { return sizeof(uint4) * row_vecs(K); }
 constexpr size_t decode_fixed_bytes(int group, int E) {
   return decode_ring_bytes(group) + sizeof(float) * kDWarps * kSums * 32 +
          sizeof(int) * (2 * (E + 1) + 4 * kDRows + 4);
 }
-// Rows of X that fit beside the rest (an even number, at most kDRows).
+// Rows of X that fit beside the rest, at most kDRows.
 int decode_rows(int group, int K, int E) {
   const size_t fixed = decode_fixed_bytes(group, E);
   if (fixed >= kDecodeSmem) return 0;
-  return static_cast<int>(std::min<size_t>(kDRows, (kDecodeSmem - fixed) / decode_row_bytes(K))) & ~1;
+  return static_cast<int>(std::min<size_t>(kDRows, (kDecodeSmem - fixed) / decode_row_bytes(K)));
 }
 
 // The expert of an entry: the last e with first[e] <= entry.
@@ -513,13 +493,12 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
   uint4* const ring = smem;
   uint4* const panel = ring + decode_ring_bytes(GROUP) / sizeof(uint4);           // [cap] rows
   float* const red = reinterpret_cast<float*>(panel + cap * row_vecs(A.K));       // [warp][kSums][lane]
-  float* const less = red + kDWarps * kSums * 32;   // [K / 32][cap]: -136 times a row's sums
-  int* const offs = reinterpret_cast<int*>(less + cap * (A.K / 32));   // [E + 1]
+  int* const offs = reinterpret_cast<int*>(red + kDWarps * kSums * 32);           // [E + 1]
   int* const first = offs + A.E + 1;      // [E + 1] first entry of each expert
   int* const c_expert = first + A.E + 1;  // of each entry at hand: its expert,
   int* const c_row = c_expert + kDRows;   // its first row,
   int* const c_rows = c_row + kDRows;     // its rows,
-  int* const c_at = c_rows + kDRows;      // their (even) place in the panel; [count] ends it
+  int* const c_at = c_rows + kDRows;      // their place in the panel; [count] ends it
   int* const c_end = c_at + kDRows + 1;   // the first item past the entries at hand
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -567,7 +546,7 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
         c_row[n] = row;
         c_rows[n] = rows;
         c_at[n] = at;
-        at += (rows + 1) & ~1;
+        at += rows;
         ++n;
       }
       c_at[n] = at;
@@ -604,7 +583,7 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
     const int nv = A.K / 8, rows = c_at[entries];
     for (int j = warp, i = 0; j < rows; j += kDWarps) {
       while (j >= c_at[i + 1]) ++i;
-      int row = c_row[i] + min(j - c_at[i], c_rows[i] - 1);
+      int row = c_row[i] + j - c_at[i];
       if (GATE_UP && A.perm) row = __ldg(A.perm + row) / A.top_k;
       if (!index_ok(row >= 0 && row < A.x_rows)) row = 0;
       const uint4* from = reinterpret_cast<const uint4*>(A.x) + static_cast<long long>(row) * nv;
@@ -614,22 +593,8 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    const int kg = A.K / 32;
-    for (int j = threadIdx.x; j < rows * kg; j += kDThreads) {
-      const int h = j / rows, r = j - h * rows;   // neighbouring threads in different rows' banks
-      float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float f[8];
-        unpack8(panel[r * row_vecs(A.K) + 4 * h + v], f);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) sum += f[q];
-      }
-      less[h * cap + r] = -136.f * sum;
-    }
-    __syncthreads();
 
-    float acc[2][4];
+    float acc[2][1][4];
     int item = 0, run = 0, k = 0;
     auto finish = [&]() {   // acc is the whole of `item`
       const int entry = (c0 + item) / A.nt, i = entry - entry0;
@@ -642,11 +607,11 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (GATE_UP) {
-            const float G = acc[m][q], U = acc[m][q + 2];
+            const float G = acc[m][0][q], U = acc[m][0][q + 2];
             row[16 * it + 8 * m + g] = __float2bfloat16(__fdividef(G, 1.f + __expf(-G)) * U);
           } else {
-            row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][q]);
-            row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][q + 2]);
+            row[32 * it + 16 * m + g] = __float2bfloat16(acc[m][0][q]);
+            row[32 * it + 16 * m + g + 8] = __float2bfloat16(acc[m][0][q + 2]);
           }
         }
       }
@@ -658,10 +623,8 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
       const int i = (c0 + item) / A.nt - entry0;
       const int row = c_at[i] + min(g, c_rows[i] - 1);   // past the last row: that row
       const uint4* xk = panel + row * row_vecs(A.K) + c + 8 * k;
-      // the lane's two rows (within the panel's places even past the last row)
-      const float* lk = less + 2 * k * cap + min(c_at[i] + 2 * c, cap - 2);
 #pragma unroll
-      for (int j = 0; j < kSums; ++j) acc[j / 4][j % 4] = 0.f;
+      for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] = 0.f;
       for (int left = run; left > 0; left -= kStageTiles) {
         const int slot = stream.slot + 1 == kStages ? 0 : stream.slot + 1;   // the oldest stage
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -675,17 +638,15 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
           const uint4 a = stage[64 * p + lane], b = stage[64 * p + 32 + lane];
           const uint2 s0 = sc[scale_step(GROUP) * p];
           const uint2 s1 = GROUP == 32 ? sc[scale_step(GROUP) * p + 8] : s0;
-          half_tile_less(a.x, a.y, b.x, b.y, xk[8 * p],
-                         *reinterpret_cast<const float2*>(lk + 2 * p * cap), s0, acc);
-          half_tile_less(a.z, a.w, b.z, b.w, xk[8 * p + 4],
-                         *reinterpret_cast<const float2*>(lk + (2 * p + 1) * cap), s1, acc);
+          const uint4 x0[1] = {xk[8 * p]}, x1[1] = {xk[8 * p + 4]};
+          half_tile<1>(a.x, a.y, b.x, b.y, x0, s0, acc);
+          half_tile<1>(a.z, a.w, b.z, b.w, x1, s1, acc);
         }
         xk += 8 * kStageTiles;
-        lk += 2 * kStageTiles * cap;
       }
       if (k != 0) {   // the end, or the middle, of an item begun by an earlier warp
 #pragma unroll
-        for (int j = 0; j < kSums; ++j) red[(warp * kSums + j) * 32 + lane] = acc[j / 4][j % 4];
+        for (int j = 0; j < kSums; ++j) red[(warp * kSums + j) * 32 + lane] = acc[j / 4][0][j % 4];
       } else if (run == kt) {
         finish();
       }
@@ -698,7 +659,7 @@ __global__ void __launch_bounds__(kDThreads, 1) w4_decode_kernel(W4Args A, int c
         const int n = min(need, piece(w + 1) - piece(w));
         if (n > 0) {
 #pragma unroll
-          for (int j = 0; j < kSums; ++j) acc[j / 4][j % 4] += red[(w * kSums + j) * 32 + lane];
+          for (int j = 0; j < kSums; ++j) acc[j / 4][0][j % 4] += red[(w * kSums + j) * 32 + lane];
         }
         need -= n;
       }
@@ -759,15 +720,24 @@ int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
 
 // The persistent kernel is for few rows per expert (mean, rounded up) and enough
 // k-tiles to share; its measured times against the other kernel's, both products:
-//   1 row  (16 tokens, 128 experts, K 8, d 2048, I 768)   48 : 58 us
-//   4 rows (64 tokens)                                    65 : 83 us
-//   8 rows (128 tokens)                                   87 : 97 us
-//   12 rows (128 tokens, 64 experts, K 6, I 1408)        109 : 107 us
-// and by the k-tiles of the gate and up products, at most 1 row:
-//   33 K (1 token, 32 experts, K 4, d 4096, I 2048)       21 : 22 us
-//   12 K (1 token, 128 experts, K 8, d 2048, I 768)       15 : 12 us
-constexpr int kDecodeRows = 8;
-constexpr int kDecodeTiles = 20000;
+//   1 row   (16 tokens, 128 experts, K 8, d 2048, I 768)    48 : 56 us
+//   4 rows  (64 tokens)                                     65 : 81 us
+//   8 rows  (128 tokens)                                    87 : 97 us
+//   12 rows (192 tokens)                                   115 : 118 us
+//   16 rows (256 tokens)                                   142 : 144 us
+//   16 rows (128 tokens, 32 experts, K 4, d 4096, I 2048)  172 : 179 us
+//   32 rows (256 tokens)                                   315 : 280 us
+// and by the k-tiles of a product at less than 1 row. The gate and up product
+// starts behind the kernel's reading of the row counts, the down product does that
+// while the first one ends, so they pay from different counts on:
+//   gate and up 25 K (2 tokens, 128 experts)    18.0 : 15.8 us
+//               33 K (1 token, 32 experts)      21.7 : 20.0 us
+//               37 K (3 tokens, 128 experts)    21.4 : 21.8 us
+//   down        25 K (4 tokens, 128 experts)    25.9 : 27.3 us
+//               33 K (2 tokens, 32 experts)     30.1 : 32.0 us
+constexpr int kDecodeRows = 16;
+constexpr int kGateUpTiles = 36000;
+constexpr int kDownTiles = 20000;
 
 // most_rows: a bound on the rows of one expert.
 template <bool GATE_UP>
@@ -777,8 +747,8 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
   const long long entries = a.E + a.M / 8;   // at most
   const int cap = decode_rows(a.group, a.K, a.E);
   const long long k_tiles = static_cast<long long>(slots) * a.nt * (a.K / 64);
-  if (mean_rows <= kDecodeRows && k_tiles >= kDecodeTiles && cap >= 8 &&
-      entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
+  if (mean_rows <= kDecodeRows && k_tiles >= (GATE_UP ? kGateUpTiles : kDownTiles) &&
+      cap >= 8 && entries * a.nt * (a.K / 64) < 0x7fffffffLL) {
     ProfScope prof(name, st);
     if (a.group == 32) return launch_decode<GATE_UP, 32>(a, cap, st);
     if (a.group == 64) return launch_decode<GATE_UP, 64>(a, cap, st);
@@ -799,11 +769,12 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
     return launch_split<GATE_UP, N, 128>(S, grid, a, st);
   };
   // Rows of a pass: the weights are read again for every 8, 16 or 32 rows of an
-  // expert, and the wider passes leave room for fewer warps. 64 tokens at 128
-  // experts (4 rows) 83, 86 and 86 us with 8, 16 and 32 rows a pass; 256 tokens (16
-  // rows) 147 us with 32, where 8 rows a pass would read the weights twice.
+  // expert, and the wider passes leave room for fewer warps. 128 experts, K 8,
+  // d 2048, I 768, with 8, 16 and 32 rows a pass: 4 rows per expert 81, 83 and 85 us,
+  // 8 rows 108, 97 and 99 us, 16 rows 170, 144 and 146 us, 24 rows 215, 179 and
+  // 175 us, 32 rows 379, 307 and 280 us.
   if (mean_rows <= 6) return by_group(std::integral_constant<int, 1>());
-  if (mean_rows <= 12) return by_group(std::integral_constant<int, 2>());
+  if (mean_rows <= 16) return by_group(std::integral_constant<int, 2>());
   return by_group(std::integral_constant<int, 4>());
 }
 

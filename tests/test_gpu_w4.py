@@ -83,12 +83,46 @@ def test_quantize(E, Kd, N, group):
     (24, 2048, 768, 128, 32, [8] * 24),
     (300, 1152, 128, 64, 32, [i % 3 for i in range(300)]),
     (12, 4096, 1024, 128, 128, [5, 0, 7, 8, 1, 1, 9, 0, 2, 3, 4, 6]),
+    (40, 1024, 1408, 64, 64, [i * 5 % 9 for i in range(39)] + [17]),
+    (32, 1024, 1408, 64, 32, [i * 7 % 19 for i in range(32)]),            # up to 16 rows an entry
+    (24, 1152, 1472, 128, 32, [16, 17, 8, 0] * 5 + [33, 1, 15, 9]),
 ])
 def test_ffn(E, d, I, g_gu, g_d, counts):
     vals, wgu, wd = _experts([E, d, I], E, d, I, g_gu, g_d)
     offsets = np.concatenate([[0], np.cumsum(counts)])
     x = O.round_bf16(np.random.default_rng(d).normal(size=(offsets[-1], d)))
     _check(x, offsets, vals, wgu, wd)
+
+
+@pytest.mark.parametrize("E,d,I,rows", [(2, 256, 128, 5), (24, 2048, 768, 8), (40, 1024, 1408, 3)])
+def test_large_elements_under_codes_of_eight(E, d, I, rows):
+    """Elements 2^12 times the others whose weights are zero leave nothing in the sums."""
+    rng = np.random.default_rng([E, d])
+    at = np.arange(7, d, 256)
+    mats = [_matrix(rng, E, I, d, 64), _matrix(rng, E, I, d, 64), _matrix(rng, E, d, I, 64)]
+    for codes, _ in mats[:2]:
+        codes[:, :, at] = 8
+    wgu = B.moe_w4_pack_weights(*_plain(mats[0]), *_plain(mats[1]))
+    wd = B.moe_w4_pack_weights(*_plain(mats[2]))
+    x = rng.normal(size=(E * rows, d))
+    x[:, at] *= 4096.0
+    _check(O.round_bf16(x), np.arange(E + 1) * rows, [K.w4_values(*m) for m in mats], wgu, wd)
+
+
+@pytest.mark.parametrize("E,d,I,rows", [(2, 256, 128, 5), (24, 2048, 768, 8), (2, 256, 128, 20)])
+def test_rows_that_are_not_finite_stay_apart(E, d, I, rows):
+    """A row with an infinity and one with a NaN: not finite themselves, the others' bits kept."""
+    _, wgu, wd = _experts([E, d, 1], E, d, I, 64, 64)
+    x = O.round_bf16(np.random.default_rng(d).normal(size=(E * rows, d)))
+    offsets = to_dev(np.arange(E + 1) * rows, I32)
+    y, h = B.moe_grouped_ffn_w4(to_dev(x, BF), offsets, wgu, wd)
+    bad = [1, rows + 2]
+    x[bad[0], 3], x[bad[1], d - 1] = np.inf, np.nan
+    y2, h2 = B.moe_grouped_ffn_w4(to_dev(x, BF), offsets, wgu, wd)
+    rest = torch.ones(E * rows, dtype=torch.bool, device=y.device)
+    rest[bad] = False
+    assert torch.equal(y[rest], y2[rest]) and torch.equal(h[rest], h2[rest])
+    assert not torch.isfinite(y2[bad].float()).any()
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 4), (1, 4, 4), (3, 2, 16), (16, 6, 8), (64, 2, 8)])
