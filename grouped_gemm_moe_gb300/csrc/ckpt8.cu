@@ -23,8 +23,8 @@
 // an eighth of that rate and would bound the kernels that write more than they read.
 //
 // Measured on one GB300, a call of both directions in turn (HBM floor at 6.8 TB/s):
-//   rows 16384 x 2048 packed, dispatched to 6 experts each    83 us (80)
-//   [G | U] 65536 x 1536 packed, restored with H             113 us (105)
+//   rows 16384 x 2048 packed, dispatched to 6 experts each    82 us (80)
+//   [G | U] 65536 x 1536 packed, restored with H             112 us (105)
 //   combine gradient, 8191 tokens, K = 8, d = 2048            77 us (65)
 #include <algorithm>
 

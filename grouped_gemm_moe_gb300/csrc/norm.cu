@@ -27,9 +27,9 @@
 // atomics, the same bits every run.
 //
 // Measured on one GB300, device time a call (HBM floor at 6.8 TB/s in brackets):
-//   norm_in           32768 x 4096                        82 us (79); 2.0 us for one row
+//   norm_in           32768 x 4096                        82 us (79); 1.9 us for one row
 //   norm_out          8192 x 2048, K = 8, channel gate    57 us (54); 3.2 us for 16 rows
-//   norm_in_backward  32768 x 4096 with the residual     156 us (158)
+//   norm_in_backward  32768 x 4096 with the residual     157 us (158)
 //   norm_out_backward 16383 x 2056, gate per 1000 rows    46 us (30): 4 us of it the join
 //                     and about 4 more the spans' partial sums; 36 us at 2048 without a gate
 #include <algorithm>

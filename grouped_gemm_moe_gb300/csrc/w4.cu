@@ -723,18 +723,19 @@ int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
 //   1 row   (16 tokens, 128 experts, K 8, d 2048, I 768)    48 : 56 us
 //   4 rows  (64 tokens)                                     65 : 81 us
 //   8 rows  (128 tokens)                                    87 : 97 us
-//   12 rows (192 tokens)                                   115 : 118 us
-//   16 rows (256 tokens)                                   142 : 144 us
-//   16 rows (128 tokens, 32 experts, K 4, d 4096, I 2048)  172 : 179 us
+//   12 rows (192 tokens)                                   116 : 118 us
+//   16 rows (256 tokens)                                   143 : 144 us
+//   16 rows (256 tokens, 64 experts, K 4, I 1408)          134 : 141 us
+//   16 rows (128 tokens, 32 experts, K 4, d 4096, I 2048)  174 : 179 us
 //   32 rows (256 tokens)                                   315 : 280 us
 // and by the k-tiles of a product at less than 1 row. The gate and up product
 // starts behind the kernel's reading of the row counts, the down product does that
 // while the first one ends, so they pay from different counts on:
 //   gate and up 25 K (2 tokens, 128 experts)    18.0 : 15.8 us
 //               33 K (1 token, 32 experts)      21.7 : 20.0 us
-//               37 K (3 tokens, 128 experts)    21.4 : 21.8 us
-//   down        25 K (4 tokens, 128 experts)    25.9 : 27.3 us
-//               33 K (2 tokens, 32 experts)     30.1 : 32.0 us
+//               37 K (3 tokens, 128 experts)    20.8 : 21.8 us
+//   down        25 K (4 tokens, 128 experts)    25.5 : 27.3 us
+//               33 K (2 tokens, 32 experts)     29.7 : 32.0 us
 constexpr int kDecodeRows = 16;
 constexpr int kGateUpTiles = 36000;
 constexpr int kDownTiles = 20000;
