@@ -785,7 +785,7 @@ def _gate_args(gate: Optional[torch.Tensor], span: Optional[int], T: int, d: int
     if span < 1 or cols not in (1, d) or rows != -(-T // span) or gate.device != dev:
         raise ValueError(f"gate must be [ceil({T} / span), 1 or {d}] on {dev}, got "
                          f"{tuple(gate.shape)} with span {span}")
-    return span, cols
+    return min(span, max(T, 1)), cols   # past T it means the same, and 32 bits hold this
 
 
 def moe_norm_out(y: torch.Tensor, resid: torch.Tensor, gain: Optional[torch.Tensor] = None,
