@@ -160,6 +160,9 @@ def _need(t: torch.Tensor, dtype, ndim: int, name: str):
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    # ctypes would cut a larger size to its low 32 bits; the cheap test comes first
+    if t.numel() > 0x7fffffff and max(t.shape) > 0x7fffffff:
+        raise ValueError(f"{name}: sizes are 31 bits at most, got {tuple(t.shape)}")
 
 
 def workspace_size(op: int, T: int, E: int, K: int, R: int = 1, d: int = 0, I: int = 0) -> int:

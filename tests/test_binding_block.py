@@ -16,3 +16,31 @@ def test_a_span_past_the_tokens_means_one_gate_row(monkeypatch, span, cols):
     got, got_cols = B._gate_args(torch.ones(1, cols), span, T, d, torch.device("cpu"))
     assert got_cols == cols
     assert T <= got < 2 ** 31      # token T - 1 is in row 0, and the number fits an int
+
+
+class _OnGpu(torch.Tensor):
+    """A tensor without storage that says it is on a GPU."""
+    is_cuda = True
+
+
+def _large(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="meta").as_subclass(_OnGpu)
+
+
+@pytest.mark.parametrize("rows", [2 ** 31, 2 ** 32, 2 ** 32 + 5])
+def test_more_rows_than_31_bits_are_refused(rows):
+    """Cut to 32 bits, 2^32 rows would be none and 2^32 + 5 five: a call that returns without
+    error and without having written its outputs."""
+    x = _large(rows, 8)
+    gain = _large(8, dtype=torch.float32)
+    q, s = _large(rows, 8, dtype=torch.int8), _large(rows, 1)
+    for call in (lambda: B.moe_norm_in(x, gain),
+                 lambda: B.moe_norm_in_backward(x, x, gain, gain),
+                 lambda: B.moe_norm_out(x, x, gain),
+                 lambda: B.moe_norm_out_backward(x, x, gain, gain),
+                 lambda: B.moe_ckpt8_pack(x),
+                 lambda: B.moe_ckpt8_dispatch(q, s),
+                 lambda: B.moe_ckpt8_swiglu(q, s),
+                 lambda: B.moe_dispatch(x, gain, 1)):
+        with pytest.raises(ValueError, match="31 bits"):
+            call()
