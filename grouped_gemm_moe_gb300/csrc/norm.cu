@@ -463,7 +463,7 @@ ChunkPlan plan_chunks(int T, const RowPlan& p, int resident) {
   const long long most = static_cast<long long>(num_sms()) * resident * p.groups;
   ChunkPlan c;
   c.chunk = static_cast<int>(std::max(1LL, (T + most - 1) / most));
-  c.workers = (T + c.chunk - 1) / c.chunk;
+  c.workers = (T - 1) / c.chunk + 1;   // T >= 1, up to 2^31 - 1
   c.grid = (c.workers + p.groups - 1) / p.groups;
   return c;
 }

@@ -521,8 +521,8 @@ int moe_grouped_ffn_fp8(const moe_bf16* xp, const int32_t* offsets, int E, int M
 
 /* ------------------------------------------------------------------------
  * The block around the layer: RMS norms before and after it, with the gate, the
- * residual scale and the residual add. d % 8 == 0, d <= 16384; vectors and
- * statistics are fp32. Results are the same bits on every run (fixed summation
+ * residual scale and the residual add. d % 8 == 0, d <= 16384, T < 2^31 where no
+ * other limit is given; vectors and statistics are fp32. Results are the same bits on every run (fixed summation
  * orders, no atomics).
  * ------------------------------------------------------------------------ */
 
