@@ -27,7 +27,12 @@ int current_device() {
 }
 }  // namespace
 
-void set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<int>(e); }
+// The runtime keeps a failed call's error until it is asked for; left there, the
+// next launch's check would report it for a call that succeeded.
+void set_last_cuda_error(cudaError_t e) {
+  g_last_cuda_error = static_cast<int>(e);
+  cudaGetLastError();
+}
 
 namespace {
 struct ProfRec {
