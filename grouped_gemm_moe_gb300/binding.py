@@ -785,7 +785,8 @@ def _gate_args(gate: Optional[torch.Tensor], span: Optional[int], T: int, d: int
     if span is None:
         span = max(T, 1) if rows == 1 else 1
     span = int(span)
-    if span < 1 or cols not in (1, d) or rows != -(-T // span) or gate.device != dev:
+    fits = rows == -(-T // span) or (T == 0 and rows == 1)   # an empty batch keeps its one gate
+    if span < 1 or cols not in (1, d) or not fits or gate.device != dev:
         raise ValueError(f"gate must be [ceil({T} / span), 1 or {d}] on {dev}, got "
                          f"{tuple(gate.shape)} with span {span}")
     return min(span, max(T, 1)), cols   # past T it means the same, and 32 bits hold this
@@ -807,7 +808,10 @@ def moe_norm_out(y: torch.Tensor, resid: torch.Tensor, gain: Optional[torch.Tens
     dev = resid.device
     if dy != d or (rows % T if T else rows) or y.device != dev:
         raise ValueError(f"y must be [T*K, {d}] with T = {T} on {dev}, got {(rows, dy)} on {y.device}")
-    K = rows // T if T else 1
+    if T:
+        K = rows // T
+    else:   # an empty batch
+        K = topk_w.shape[1] if topk_w is not None and topk_w.dim() == 2 else 1
     _shaped(gain, torch.float32, (d,), "gain", dev)
     _shaped(topk_w, torch.float32, (T, K), "topk_w", dev)
     _shaped(inv_perm, torch.int32, (T * K,), "inv_perm", dev)
@@ -853,6 +857,8 @@ def moe_norm_out_backward(dout: torch.Tensor, zsum: torch.Tensor, rstd: Optional
         _shaped(out[1], torch.float32, (d,), "dgain", dev)
         _shaped(out[2], torch.float32, tuple(gate.shape) if gate is not None else (), "dgate", dev)
     dz, dgain, dgate = out
+    if T == 0 and gate is not None and dgate is not None:
+        dgate.zero_()   # the C call sees no gate rows then
     _check("moe_norm_out_backward", load().moe_norm_out_backward(
         _ptr(dout), _ptr(zsum), _ptr(rstd), _ptr(gain), _ptr(gate), span, cols, float(scale), T, d,
         _ptr(dz), _ptr(dgain), _ptr(dgate), _ptr(ws), ws.numel() * ws.element_size(),

@@ -42,3 +42,24 @@ def test_the_most_rows_an_int_holds():
     B.moe_norm_out(xn, x, gain, out=(x, None, None))     # in place on the residual stream
     want, _, _ = K.norm_out(f64(normed), f64(ends), f64(gain), None, None, 1, None, None, 1, 1.0, EPS)
     assert_bf16_close(f64(torch.cat([x[:n], x[-n:]])), want, "out")
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+@pytest.mark.parametrize("cols", [1, 64])
+def test_an_empty_batch_keeps_its_shapes(rows, cols):
+    """No tokens, K = 8: what a batch that routed nothing passes on, with a gate per channel or
+    one for the model (one row) or per token (no row); its sums are zero."""
+    d, k = 64, 8
+    none = torch.empty(0, d, dtype=BF, device=dev())
+    gain, gate = torch.ones(d, device=dev()), torch.ones(rows, cols, device=dev())
+    w, inv = torch.empty(0, k, device=dev()), torch.empty(0, dtype=I32, device=dev())
+    out, z, r = B.moe_norm_out(none, none, gain, w, inv, none, gate)
+    assert out.shape == (0, d) and z.shape == (0, d) and r.shape == (0,)
+    dgate = torch.full_like(gate, 7.0)
+    dgain = torch.full_like(gain, 7.0)
+    B.moe_norm_out_backward(none, none, r, gain, gate, out=(none, dgain, dgate))
+    assert (dgate == 0).all() and (dgain == 0).all()
+    _, _, dgate = B.moe_norm_out_backward(none, none, None, None, gate)
+    assert (dgate == 0).all()
+    with pytest.raises(ValueError):
+        B.moe_norm_out(none, none, gain, gate=torch.ones(2, cols, device=dev()))
