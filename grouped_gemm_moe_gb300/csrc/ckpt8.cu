@@ -361,12 +361,6 @@ swiglu8_kernel(const uint2* __restrict__ q, const uint16_t* __restrict__ s, Tile
 constexpr int kCbVecs = 4;
 constexpr int kCbWarps = 4;
 
-// mul_bf16_exact's rounding to odd, but an infinite factor gives infinity.
-__device__ __forceinline__ float product_to_odd(float a, float b) {
-  const float pz = __fmul_rz(a, b);
-  return __uint_as_float(__float_as_uint(pz) | (fabsf(fmaf(a, b, -pz)) > 0.f ? 1u : 0u));
-}
-
 __global__ void __launch_bounds__(kCbWarps * 32)
 combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict__ q,
                          const uint16_t* __restrict__ s, const float* __restrict__ w,
@@ -425,8 +419,8 @@ combine_backward8_kernel(const uint4* __restrict__ dout, const uint2* __restrict
 #pragma unroll                                     // multiplies the sum
         for (int k = 0; k < 8; k += 2) {
           part2 = fma_pair(make_pair(fd[u][k], fd[u][k + 1]), decode2(k < 4 ? b0 : b1, k & 3), part2);
-          g[k] = product_to_odd(wj, fd[u][k]);
-          g[k + 1] = product_to_odd(wj, fd[u][k + 1]);
+          g[k] = mul_bf16_exact(wj, fd[u][k]);
+          g[k + 1] = mul_bf16_exact(wj, fd[u][k + 1]);
         }
         const float2 both = split_pair(part2);
         float part = both.x + both.y;

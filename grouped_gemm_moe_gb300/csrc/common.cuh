@@ -110,11 +110,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Boldo and Melquiond, "Emulation of FMA and correctly rounded sums: proved
 // algorithms using rounding to odd" (IEEE Trans. Computers, 2008). The residual
 // is exact while it is representable, i.e. for |a*b| above about 2^-103; below
-// that a nonzero residual can round to zero and the odd bit be missed.
+// that a nonzero residual can round to zero and the odd bit be missed. An infinite
+// product has the residual NaN, which the comparison leaves alone.
 __device__ __forceinline__ float mul_bf16_exact(float a, float b) {
   const float pz = __fmul_rz(a, b);
   const float r = fmaf(a, b, -pz);
-  return __uint_as_float(__float_as_uint(pz) | (r != 0.f ? 1u : 0u));
+  return __uint_as_float(__float_as_uint(pz) | (fabsf(r) > 0.f ? 1u : 0u));
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
