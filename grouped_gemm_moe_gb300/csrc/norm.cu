@@ -1017,7 +1017,9 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
   };
   auto by_k = [&](auto v) {
     constexpr int N = decltype(v)::value;
-    if (K == 1) return go(norm_out_kernel<1, N>);
+    if constexpr (N == 8) {   // shorter rows of one slot always fit a ring
+      if (K == 1) return go(norm_out_kernel<1, N>);
+    }
     if (K <= 2) return go(norm_out_kernel<2, N>);
     if (K <= 4) return go(norm_out_kernel<4, N>);
     return go(norm_out_kernel<8, N>);
