@@ -51,6 +51,10 @@ class LayerScratch:
         if shared_I:
             self.xs, self.ys, self.dxs = e(T, d), e(T, d), e(T, d)
             self.hs, self.gus = e(T, shared_I), e(T, 2 * shared_I)
+            self.ws_sfwd = B.new_workspace(
+                B.workspace_size(B.MOE_OP_GROUPED_FFN, T, 1, 1, 1, d, shared_I), device)
+            self.ws_sbwd = B.new_workspace(
+                B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, 1, 1, 1, d, shared_I), device)
 
 
 class MoELayer:
@@ -120,15 +124,16 @@ class MoELayer:
             self.s_offsets = torch.tensor([0, T], dtype=i32, device=dev)
             if scratch is not None:
                 self.ys, self.hs, self.gus = scratch.ys, scratch.hs, scratch.gus
-                self.dxs = scratch.dxs
+                self.dxs, self.ws_sfwd, self.ws_sbwd = scratch.dxs, scratch.ws_sfwd, scratch.ws_sbwd
             else:
                 self.ys, self.hs, self.gus = e(T, d, dt=bf), e(T, Is, dt=bf), e(T, 2 * Is, dt=bf)
                 self.dxs = e(T, d, dt=bf)
+                self.ws_sfwd = B.new_workspace(
+                    B.workspace_size(B.MOE_OP_GROUPED_FFN, T, 1, 1, 1, d, Is), dev)
+                self.ws_sbwd = B.new_workspace(
+                    B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, 1, 1, 1, d, Is), dev)
             self.dws_gate, self.dws_up = e(1, d, Is, dt=f32), e(1, d, Is, dt=f32)
             self.dws_down = e(1, Is, d, dt=f32)
-            self.ws_sfwd = B.new_workspace(B.workspace_size(B.MOE_OP_GROUPED_FFN, T, 1, 1, 1, d, Is), dev)
-            self.ws_sbwd = B.new_workspace(
-                B.workspace_size(B.MOE_OP_GROUPED_FFN_BACKWARD, T, 1, 1, 1, d, Is), dev)
         self.aux_loss_coef = float(aux_loss_coef)
         if self.aux_loss_coef > 0:
             self.lb_frac, self.lb_pmean, self.lb_stats = e(E, dt=f32), e(E, dt=f32), e(4, dt=f32)
@@ -163,6 +168,8 @@ class MoELayer:
     # -------------------------------------------------------------- passes
     def forward(self, logits: torch.Tensor, x: torch.Tensor, copy_splits: bool = True):
         y, topk_w, inv_perm, shared_y = self.experts(logits, x, copy_splits)
+        if self.out is None:      # a block around this layer gave it up
+            self.out = torch.empty(self.T, self.d, dtype=torch.bfloat16, device=self.device)
         self._run("combine", B.moe_combine, y, topk_w, inv_perm, shared_y, out=self.out)
         return self.out
 

@@ -536,7 +536,7 @@ int moe_norm_in(const moe_bf16* x, const float* gain, int T, int d, float eps, m
  * u = gain dxn,
  *   dx = bf16(dres + r (u - xh mean_c(u xh))),  dgain = sum_t dxn xh.
  *   dxn, x [T,d] bf16, gain [d], rstd [T] in; dres [T,d] bf16 or NULL (zero).
- *   dx [T,d] bf16 out; dgain [d] fp32 out (written, zero when T == 0).
+ *   dx [T,d] bf16 out, may be dres; dgain [d] fp32 out (written, zero when T == 0).
  *   ws: moe_workspace_size(MOE_OP_NORM_BACKWARD, T, 1, 1, 1, d, 0) bytes. T <= 2^30. */
 int moe_norm_in_backward(const moe_bf16* dxn, const moe_bf16* x, const float* gain,
                          const float* rstd, const moe_bf16* dres, int T, int d, moe_bf16* dx,
