@@ -46,8 +46,10 @@ struct ProfScope {
 
 // Launches a kernel with programmatic dependent launch: it may be scheduled
 // while the previous kernel of the stream is still finishing, so it must run
-// pdl_wait() before it reads anything an earlier launch wrote (every kernel of
-// this library does so first thing). cluster_x > 1 adds a cluster dimension.
+// pdl_wait() before it reads anything an earlier launch wrote, and before it ends
+// (every kernel of this library waits first thing but the persistent 4-bit down
+// projection, which first reads what is older than a launch that has itself waited).
+// cluster_x > 1 adds a cluster dimension.
 template <typename... KArgs, typename... Args>
 inline int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                       unsigned cluster_x, const Args&... args) {

@@ -32,6 +32,12 @@
 //   norm_in_backward  32768 x 4096 with the residual     157 us (158)
 //   norm_out_backward 16383 x 2056, gate per 1000 rows    46 us (30): 4 us of it the join
 //                     and about 4 more the spans' partial sums; 36 us at 2048 without a gate
+//   norm_out_backward 32768 x 4096, no gate, one for the model, one per channel
+//                     123, 131 and 127 us (118): a gate of one column sums a span's rows in
+//                     one block, on one SM
+// Rows above d = 8192 are further from it. The gradients' four vectors a thread spill (160 to
+// 650 bytes): 16384 x 8200 with the residual 357 us (158), 290 without gate and 375 with one
+// per channel (119); 8192 x 16384 349 (158), 244 and 311 (118).
 #include <algorithm>
 
 #include "common.cuh"
@@ -992,6 +998,13 @@ extern "C" int moe_norm_out(const moe_bf16* y, const float* topk_w, const int32_
   auto yi = reinterpret_cast<const uint4*>(y), si = reinterpret_cast<const uint4*>(shared_y);
   auto ri = reinterpret_cast<const uint4*>(resid);
   auto oo = reinterpret_cast<uint4*>(out), zo = reinterpret_cast<uint4*>(zsum);
+  // A ring of two stages, of four where a row has four arrays at most; without one the
+  // gathers stay in registers. The ring is faster where it fits: 8192 x 2048, K 8 57 us
+  // against 68, 4096 x 6144, K 8 84 against 113. Its 16 S arrays G bytes pass 226 KB above
+  // d = 6400 with K 8 (5632 with shared rows): 4096 x 8192, K 8 130 us (floor 109), with
+  // shared rows 157 (118); K 32 at 4096 x 2048 100 (86); 4096 x 16384, K 2 149 (99). Four
+  // arrays above d = 7168 take registers too, although two stages would fit and be faster:
+  // 8192 x 8192, K 3 176 us against 127, K 2 with shared rows 211 against 122 (118).
   const RowPlan wide = plan_rows(d, 1);
   const int arrays = K + 1 + (shared_y ? 1 : 0);
   const int S = arrays <= 4 ? 4 : 2;

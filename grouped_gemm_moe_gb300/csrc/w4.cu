@@ -12,9 +12,13 @@
 // lane, which feed eight m16n8k16 products whose A is the weights and whose 8
 // columns are rows of X. A code becomes the bf16 integer q - 8 in registers (exact:
 // two logic instructions and a subtraction a pair), so the products run on integers
-// and the scale multiplies the fp32 sums of a group: no weight is ever rounded. The
+// and the scale multiplies fp32 sums of 32 K: no weight is ever rounded. The
 // lane's 16 elements of K are two runs of 8, one in each half of the 64, which is
 // the order the rows of X are loaded in 16-byte pieces and keeps groups of 32 apart.
+//
+// H is rounded to bf16 between the products, as by the bf16 experts: it is an output, and
+// as the down product's 16-bit operand it takes one MMA a tile. Next to a product of the
+// unrounded H that moves y by 1.7e-3 of its norm, as much as y's own rounding does.
 //
 // mma.sync and not tcgen05: the A operand is made in registers from 4-bit codes
 // and N is 8 to 32; tcgen05 would take it through shared memory or TMEM at
@@ -736,6 +740,10 @@ int launch_decode(const W4Args& a, int cap, cudaStream_t st) {
 //               37 K (3 tokens, 128 experts)    20.8 : 21.8 us
 //   down        25 K (4 tokens, 128 experts)    25.5 : 27.3 us
 //               33 K (2 tokens, 32 experts)     29.7 : 32.0 us
+// A block has to hold an entry's 8 rows of X, which ends the persistent kernel at K = 6400 to
+// 6976 (groups of 32 to 128): gate and up of wider models take the other one. Both products,
+// 32 experts, K 4, I 2048, floor in brackets: d 6656, 16, 64 and 128 tokens 113 (90), 166 and
+// 280 us (99); d 7168 135 (97), 187 and 279 (107); d 8192 140 (103), 216 and 333 (122).
 constexpr int kDecodeRows = 16;
 constexpr int kGateUpTiles = 36000;
 constexpr int kDownTiles = 20000;
@@ -756,7 +764,9 @@ int launch_w4(const char* name, const W4Args& a, int most_rows, cudaStream_t st)
     return launch_decode<GATE_UP, 128>(a, cap, st);
   }
   // Split K until the launch has about 24 warps per SM three times over, a warp
-  // keeping four k-tiles at least.
+  // keeping four k-tiles at least. Against a third and three times of that, 32 experts,
+  // K 4, I 2048: 256 tokens of d 4096 272 us (332, 331), 128 of d 8192 333 (373, 353); a few
+  // tokens take the same time (1 of d 8192: 31 us each).
   const long long want = static_cast<long long>(num_sms()) * 72;
   const long long tiles = static_cast<long long>(slots) * a.nt;
   int S = 1;

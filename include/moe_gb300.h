@@ -585,7 +585,7 @@ int moe_norm_out_backward(const moe_bf16* dout, const moe_bf16* zsum, const floa
  *   a value that is not finite. Restored: q s, NaN for -128 (so an overflow in
  *   the forward still reaches the gradients). A value within s / 2 of bf16's
  *   largest may be restored as infinity.
- * N (d, 2 I) a multiple of 8.
+ * N is a multiple of 8 (2 I a multiple of 16: I is one of 8 itself).
  * ------------------------------------------------------------------------ */
 int moe_ckpt8_pack(const moe_bf16* x, int M, int N, int8_t* q, moe_bf16* s, void* stream);
 
