@@ -38,6 +38,8 @@ MOE_OP_GROUPED_FFN_FP8 = 7
 MOE_OP_ROUTE_PERMUTE_EP = 8
 MOE_OP_NORM_BACKWARD = 9
 MOE_OP_GROUPED_FFN_W4 = 10
+MOE_OP_GROUPED_FFN_FP4 = 11
+MOE_OP_GROUPED_GEMM_WGRAD = 12
 
 WORKSPACE_HEADER = 256
 
@@ -94,6 +96,15 @@ SIGNATURES = {
     "moe_w4_pack_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "moe_grouped_ffn_w4": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                                 _P, _SZ, _P]),
+    "moe_grouped_gemm": (_I, [_P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _SZ, _P]),
+    "moe_grouped_gemm_wgrad": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_fp4_quantize_rows": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_fp4_dequantize_rows": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_fp4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_fp4_pack_scales": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_grouped_gemm_fp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grouped_ffn_fp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P,
+                                 _P, _P, _P, _SZ, _P]),
     "moe_debug_check_status": (_I, [ctypes.POINTER(ctypes.c_int)]),
     "moe_read_device_status": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
     "moe_debug_wait_timeout": (_I, [_P, _I, _P]),
@@ -1044,6 +1055,263 @@ def moe_grouped_ffn_w4(x: torch.Tensor, offsets: torch.Tensor, wgu, wd,
         _ptr(wgu[1]), _ptr(wd[0]), _ptr(wd[1]), _ptr(y), _ptr(h), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(dev)))
     return y, h
+
+
+# ---------------------------------------------------------------- products grouped by expert
+def _call(name: str, dev: torch.device, *args):
+    """The entry point on dev's current stream, with dev the current device."""
+    fn = getattr(load(), name)
+    if dev.index == torch._C._cuda_getDevice():
+        return _check(name, fn(*args, _stream(dev)))
+    with torch.cuda.device(dev):
+        _check(name, fn(*args, _stream(dev)))
+
+
+def _experts_of(offsets: torch.Tensor, dev) -> int:
+    _need(offsets, torch.int32, 1, "offsets")
+    if offsets.numel() < 2 or offsets.device != dev:
+        raise ValueError(f"offsets must hold E + 1 entries on {dev}")
+    return offsets.numel() - 1
+
+
+def moe_grouped_gemm(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor, trans: bool = False,
+                     ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """y [M,N] bf16: expert e's rows of x [M,K] times w[e], w [E,K,N], or with trans times the
+    transpose of w[e], w [E,N,K] (the input gradient of the product without trans)."""
+    _need(x, torch.bfloat16, 2, "x")
+    _need(w, torch.bfloat16, 3, "w")
+    M, K = x.shape
+    dev = x.device
+    E = _experts_of(offsets, dev)
+    N = w.shape[1] if trans else w.shape[2]
+    _shaped(w, torch.bfloat16, (E, N, K) if trans else (E, K, N), "w", dev)
+    ws = _need_ws(ws, WORKSPACE_HEADER, dev)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _shaped(out, torch.bfloat16, (M, N), "y", dev)
+    _call("moe_grouped_gemm", dev, _ptr(x), _ptr(offsets), E, M, K, N, _ptr(w), int(bool(trans)),
+          _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    return out
+
+
+def moe_grouped_gemm_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor,
+                           accumulate: bool = False, ws: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None):
+    """dw [E,K,N] fp32: x_e^T dy_e of each expert's rows of x [M,K] and dy [M,N]; with accumulate
+    added to out, which has to be given."""
+    _need(x, torch.bfloat16, 2, "x")
+    M, K = x.shape
+    dev = x.device
+    E = _experts_of(offsets, dev)
+    _need(dy, torch.bfloat16, 2, "dy")
+    N = dy.shape[1]
+    _shaped(dy, torch.bfloat16, (M, N), "dy", dev)
+    ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_GEMM_WGRAD, M, E, 1, 1, K, N) if ws is None else 0,
+                  dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to out: give it")
+        out = torch.empty(E, K, N, dtype=torch.float32, device=dev)
+    else:
+        _shaped(out, torch.float32, (E, K, N), "dw", dev)
+    _call("moe_grouped_gemm_wgrad", dev, _ptr(x), _ptr(dy), _ptr(offsets), E, M, K, N,
+          int(bool(accumulate)), _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    return out
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floats
+def _fp4_block(block: int, K: int, name: str):
+    if block not in (16, 32):
+        raise ValueError(f"block must be 16 or 32, got {block}")
+    if K < 64 or K % 64:
+        raise ValueError(f"{name} must be a multiple of 64, got {K}")
+
+
+def _fp4_atoms(K: int, block: int) -> int:
+    return -(-K // (4 * block))
+
+
+def _fp4_rows_shapes(M: int, d: int, E: int, block: int):
+    tiles = -(-M // 128) + 2 * E
+    return (M, d // 2), (tiles, _fp4_atoms(d, block), 512), (M,)
+
+
+def _fp4_rows(rows, E: int, block: int, dev):
+    """(q, sf, row_scale, M, K) of checked rows from moe_fp4_quantize_rows."""
+    q, sf, rs = rows
+    _need(q, torch.uint8, 2, "q")
+    M, d = q.shape[0], 2 * q.shape[1]
+    _fp4_block(block, d, "K")
+    _, s_sf, s_rs = _fp4_rows_shapes(M, d, E, block)
+    _shaped(q, torch.uint8, (M, d // 2), "q", dev)
+    _need(sf, torch.uint8, 3, "sf")
+    _shaped(sf, torch.uint8, s_sf, "sf", dev)
+    if block == 16:
+        _need(rs, torch.float32, 1, "row_scale")
+        _shaped(rs, torch.float32, s_rs, "row_scale", dev)
+    else:
+        rs = None
+    return q, sf, rs, M, d
+
+
+def moe_fp4_quantize_rows(x: torch.Tensor, offsets: torch.Tensor, block: int = 16,
+                          inv_perm: Optional[torch.Tensor] = None, K: int = 1, out=None):
+    """4-bit rows (q [M,d/2] uint8, sf [tiles,KA,512] uint8, row_scale [M] fp32 or None with
+    block 32) in expert order: with inv_perm, token t of x [T,d] goes to rows inv_perm[t*K + j]
+    (M = T*K); without, x holds the rows in expert order."""
+    _need(x, torch.bfloat16, 2, "x")
+    T, d = x.shape
+    dev = x.device
+    _fp4_block(block, d, "d")
+    E = _experts_of(offsets, dev)
+    K = int(K)
+    if inv_perm is None and K != 1:
+        raise ValueError("K is the number of copies that inv_perm places: without it 1")
+    M = T * K
+    _shaped(inv_perm, torch.int32, (M,), "inv_perm", dev)
+    s_q, s_sf, s_rs = _fp4_rows_shapes(M, d, E, block)
+    if out is None:
+        out = (torch.empty(s_q, dtype=torch.uint8, device=dev),
+               torch.empty(s_sf, dtype=torch.uint8, device=dev),
+               torch.empty(s_rs, dtype=torch.float32, device=dev) if block == 16 else None)
+    else:
+        _fp4_rows(out, E, block, dev)
+        _shaped(out[0], torch.uint8, s_q, "q", dev)
+    q, sf, rs = out
+    _call("moe_fp4_quantize_rows", dev, _ptr(x), _ptr(inv_perm), T, K, _ptr(offsets), E, d, block,
+          _ptr(q), _ptr(sf), _ptr(rs) if block == 16 else None)
+    return out
+
+
+def moe_fp4_dequantize_rows(rows, offsets: torch.Tensor, block: int = 16,
+                            out: Optional[torch.Tensor] = None):
+    """The rows of moe_fp4_quantize_rows in bf16 [M,d]."""
+    dev = rows[0].device
+    E = _experts_of(offsets, dev)
+    q, sf, rs, M, d = _fp4_rows(rows, E, block, dev)
+    if out is None:
+        out = torch.empty(M, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _shaped(out, torch.bfloat16, (M, d), "out", dev)
+    _call("moe_fp4_dequantize_rows", dev, _ptr(q), _ptr(sf), _ptr(rs), _ptr(offsets), E, M, d, block,
+          _ptr(out))
+    return out
+
+
+def moe_fp4_quantize_weights(w: torch.Tensor, block: int = 16, out=None):
+    """A plain 4-bit checkpoint of w [E,K,N] bf16: codes [E,N,K/2] and scales [E,N,K/block] uint8,
+    scale [E] fp32 (None with block 32)."""
+    _need(w, torch.bfloat16, 3, "w")
+    E, K, N = w.shape
+    dev = w.device
+    _fp4_block(block, K, "K")
+    if out is None:
+        out = (torch.empty(E, N, K // 2, dtype=torch.uint8, device=dev),
+               torch.empty(E, N, K // block, dtype=torch.uint8, device=dev),
+               torch.empty(E, dtype=torch.float32, device=dev) if block == 16 else None)
+    else:
+        _shaped(out[0], torch.uint8, (E, N, K // 2), "codes", dev)
+        _shaped(out[1], torch.uint8, (E, N, K // block), "scales", dev)
+        _shaped(out[2], torch.float32, (E,), "scale", dev)
+    codes, scales, scale = out
+    _call("moe_fp4_quantize_weights", dev, _ptr(w), E, K, N, block, _ptr(codes), _ptr(scales),
+          _ptr(scale))
+    return out
+
+
+def moe_fp4_pack_scales(scales_a: torch.Tensor, scales_b: Optional[torch.Tensor] = None,
+                        block: int = 16, out: Optional[torch.Tensor] = None):
+    """Block scales [E,N,K/block] uint8 of a plain checkpoint as the products read them: sf
+    [E,tiles,KA,512] of one matrix, or of gate (a) and up (b) together."""
+    _need(scales_a, torch.uint8, 3, "scales_a")
+    E, N, K = scales_a.shape[0], scales_a.shape[1], scales_a.shape[2] * block
+    dev = scales_a.device
+    _fp4_block(block, K, "K")
+    _shaped(scales_b, torch.uint8, tuple(scales_a.shape), "scales_b", dev)
+    if N % (8 if scales_b is None else 64):
+        raise ValueError(f"N = {N} must be a multiple of {8 if scales_b is None else 64}")
+    shape = (E, -(-N // 128) if scales_b is None else N // 64, _fp4_atoms(K, block), 512)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _shaped(out, torch.uint8, shape, "sf", dev)
+    _call("moe_fp4_pack_scales", dev, _ptr(scales_a), _ptr(scales_b), E, N, K, block, _ptr(out))
+    return out
+
+
+def _fp4_factor(t: Optional[torch.Tensor], E: int, block: int, name: str, dev):
+    if block == 32:
+        return None
+    _need(t, torch.float32, 1, name)
+    _shaped(t, torch.float32, (E,), name, dev)
+    return t
+
+
+def moe_grouped_gemm_fp4(rows, offsets: torch.Tensor, w, block: int = 16,
+                         ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """y [M,N] bf16 of 4-bit rows (from moe_fp4_quantize_rows) and weights ``w`` = (codes [E,N,K/2],
+    scales from moe_fp4_pack_scales, scale [E] or None)."""
+    dev = rows[0].device
+    E = _experts_of(offsets, dev)
+    q, sf, rs, M, K = _fp4_rows(rows, E, block, dev)
+    codes, wsf, scale = w
+    _need(codes, torch.uint8, 3, "codes")
+    N = codes.shape[1]
+    _shaped(codes, torch.uint8, (E, N, K // 2), "codes", dev)
+    _shaped(wsf, torch.uint8, (E, -(-N // 128), _fp4_atoms(K, block), 512), "weight scales", dev)
+    scale = _fp4_factor(scale, E, block, "scale", dev)
+    ws = _need_ws(ws, WORKSPACE_HEADER, dev)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _shaped(out, torch.bfloat16, (M, N), "y", dev)
+    _call("moe_grouped_gemm_fp4", dev, _ptr(q), _ptr(sf), _ptr(rs), _ptr(offsets), E, M, K, N, block,
+          _ptr(codes), _ptr(wsf), _ptr(scale), _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    return out
+
+
+def moe_grouped_ffn_fp4(rows, offsets: torch.Tensor, wgu, wd, block: int = 16,
+                        h_scale: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None):
+    """y [M,d] bf16 of the SwiGLU experts on 4-bit rows and weights. ``wgu`` = (gate codes, up codes
+    [E,I,d/2], their scales packed together, gate scale, up scale [E]), ``wd`` = (codes [E,d,I/2],
+    packed scales, scale [E]); the factors are None with block 32. h_scale [E] fp32 (block 16) fixes
+    the hidden rows' factor per expert; without it each hidden row takes its own maximum."""
+    dev = rows[0].device
+    E = _experts_of(offsets, dev)
+    q, sf, rs, M, d = _fp4_rows(rows, E, block, dev)
+    gate, up, gsf, gscale, uscale = wgu
+    down, dsf, dscale = wd
+    _need(gate, torch.uint8, 3, "gate codes")
+    I = gate.shape[1]
+    if I % 64 or I < 64:
+        raise ValueError(f"I must be a multiple of 64, got {I}")
+    _shaped(gate, torch.uint8, (E, I, d // 2), "gate codes", dev)
+    _need(up, torch.uint8, 3, "up codes")
+    _shaped(up, torch.uint8, (E, I, d // 2), "up codes", dev)
+    _need(gsf, torch.uint8, 4, "gate and up scales")
+    _shaped(gsf, torch.uint8, (E, I // 64, _fp4_atoms(d, block), 512), "gate and up scales", dev)
+    _need(down, torch.uint8, 3, "down codes")
+    _shaped(down, torch.uint8, (E, d, I // 2), "down codes", dev)
+    _need(dsf, torch.uint8, 4, "down scales")
+    _shaped(dsf, torch.uint8, (E, -(-d // 128), _fp4_atoms(I, block), 512), "down scales", dev)
+    gscale, uscale, dscale = (_fp4_factor(t, E, block, n, dev) for t, n in
+                              ((gscale, "gate scale"), (uscale, "up scale"), (dscale, "down scale")))
+    if h_scale is not None:
+        if block == 32:
+            raise ValueError("h_scale goes with block 16")
+        _shaped(h_scale, torch.float32, (E,), "h_scale", dev)
+    ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_FFN_FP4, M, E, 1, 1, d, I) if ws is None else 0,
+                  dev)
+    if out is None:
+        out = torch.empty(M, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _shaped(out, torch.bfloat16, (M, d), "y", dev)
+    _call("moe_grouped_ffn_fp4", dev, _ptr(q), _ptr(sf), _ptr(rs), _ptr(offsets), E, M, d, I, block,
+          _ptr(gate), _ptr(up), _ptr(gsf), _ptr(gscale), _ptr(uscale), _ptr(down), _ptr(dsf),
+          _ptr(dscale), _ptr(h_scale), _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    return out
 
 
 def moe_profile_start(capacity: int = 4096):

@@ -25,7 +25,8 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoe_gb300_debug.so")
 SOURCES = ["api.cu", "route.cu", "permute.cu", "front.cu", "gather.cu", "ep.cu", "fp8.cu",
-           "grouped_gemm.cu", "norm.cu", "ckpt8.cu", "w4.cu"]
+           "grouped_gemm.cu", "norm.cu", "ckpt8.cu", "w4.cu", "fp4.cu",
+           "fp4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

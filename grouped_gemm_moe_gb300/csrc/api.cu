@@ -11,6 +11,8 @@ size_t permutation_workspace(long long TK, int E, int R);   // permute.cu
 size_t ffn_backward_scratch(long long M, int E, int d, int I);   // grouped_gemm.cu
 size_t load_balance_workspace(int E);                       // route.cu
 size_t ffn_fp8_scratch(long long M, int E, int d, int I);   // grouped_gemm.cu
+size_t wgrad_scratch(int E, int K, int N);                   // grouped_gemm.cu
+size_t ffn_fp4_scratch(long long M, int E, int I);           // fp4_gemm.cu
 size_t route_permute_workspace(long long TK, int E, int R);   // front.cu
 size_t norm_backward_workspace(int T, int d);               // norm.cu
 
@@ -114,6 +116,12 @@ extern "C" size_t moe_workspace_size(int op, int T, int E, int K, int R, int d, 
     case MOE_OP_GROUPED_FFN_W4:
       if (I < 64 || d < 64 || d % 64 || I % 64) return 0;
       return kWorkspaceHeader;
+    case MOE_OP_GROUPED_FFN_FP4:
+      if (I < 64 || d < 64 || d % 64 || I % 64) return 0;
+      return kWorkspaceHeader + ffn_fp4_scratch(TK, E, I);
+    case MOE_OP_GROUPED_GEMM_WGRAD:
+      if (d < 8 || d % 8 || I < 8 || I % 8) return 0;
+      return kWorkspaceHeader + wgrad_scratch(E, d, I);
     default:
       return 0;
   }
@@ -130,6 +138,8 @@ int debug_status_gemm();
 int debug_status_norm();
 int debug_status_ckpt8();
 int debug_status_w4();
+int debug_status_fp4();
+int debug_status_fp4_gemm();
 }  // namespace moe
 #endif
 
@@ -145,7 +155,8 @@ extern "C" int moe_debug_check_status(int* host_status) {
   int first = 0;
   for (int v : {debug_status_route(), debug_status_permute(), debug_status_gather(),
                 debug_status_ep(), debug_status_fp8(), debug_status_gemm(), debug_status_norm(),
-                debug_status_ckpt8(), debug_status_w4()}) {
+                debug_status_ckpt8(), debug_status_w4(), debug_status_fp4(),
+                debug_status_fp4_gemm()}) {
     if (v == MOE_ERR_CUDA) return MOE_ERR_CUDA;
     if (!first) first = v;
   }

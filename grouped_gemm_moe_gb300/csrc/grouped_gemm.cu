@@ -46,12 +46,10 @@
 //   * every mbarrier wait is bounded (a few seconds of %globaltimer); on
 //     timeout the CTA records MOE_ERR_DEVICE_TIMEOUT in the workspace status
 //     word, drains its own TMA loads and MMAs, frees TMEM and exits.
-#include <cuda.h>
 #include <type_traits>
-#include <cudaTypedefs.h>
 
-#include "common.cuh"
 #include "mxfp8.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace gemm {
@@ -68,7 +66,6 @@ enum Kind : int {
 constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int kThreads = 192;
-constexpr unsigned long long kTimeoutNs = 4000000000ull;
 
 // One zero-padded straddling step to prepare for the weight gradients: for each
 // expert whose row count is not a multiple of 16, the 16-row step that holds its
@@ -109,244 +106,15 @@ struct Params {
   int* status;             // workspace status word
   PadJob pad[2];           // BWD_DH: the weight gradients' pads of X and H (a == null: none)
   int kb_half;             // BWD_DX: k-blocks of the dG half of K (then as many of the dU half)
+  int accumulate;          // weight gradients: add to dW (an expert without rows adds nothing)
+  int pad_b;               // dW by itself: B's straddling steps are zero-padded too (maps tmB2: B in
+                           // 16-row boxes, tmC1: the pads), so an Inf or NaN in the next expert's
+                           // rows meets no zero of A
   int tag_mode;            // kTagNone, kTagWrite (data part's dH) or kTagCheck (weight part)
   uint32_t tag[kTagWords]; // the backward's scratch tag: magic, M, E, d, I, offsets (low 32 bits)
   uint8_t* hq;             // MXFP8 gate/up: E4M3 of H for the down projection (null: not fused)
   uint8_t* hsf;            //   and H's scale atoms (row tiles in the tile list's m-tile order)
 };
-
-// ----------------------------------------------------------------- PTX helpers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait for the phase of `bar` with the given parity to complete.
-// Returns false if this CTA is aborting (another role timed out) or the wait
-// itself ran past kTimeoutNs (then it raises the abort flag and the status).
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
-                                            volatile int* abort_flag, int* status,
-                                            uint64_t timeout_ns = kTimeoutNs) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer() - t0 > timeout_ns) {
-        *abort_flag = 1;
-        report_status(status, MOE_ERR_DEVICE_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-// Fast path inline (the phase is usually complete already), slow path out of line.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                         int* status) {
-  if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, abort_flag, status);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// 32 lanes x 16 consecutive 32-bit columns: thread i gets row (lane base + i).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 32 lanes x 32 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// Bulk tensor store shared -> global (2-D tile), tracked by this thread's bulk groups.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(src)
-      : "memory");
-}
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y,
-                                             int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(z), "r"(src)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// This thread's committed bulk stores have finished reading shared memory.
-__device__ __forceinline__ void bulk_wait_read_all() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// At most one of this thread's committed bulk store groups is still reading shared memory.
-__device__ __forceinline__ void bulk_wait_read_1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-// This thread's committed bulk stores are complete.
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-// Orders this thread's generic-proxy shared-memory accesses with later async-proxy ones.
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// ---- CTA-pair (cluster of two, tcgen05 cta_group::2) helpers
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_id_x() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t n_clusters_x() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
-  return r;
-}
-// shared::cluster address of the same shared-memory offset in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
-}
-// TMA load into this CTA's shared memory whose completion is counted on an
-// mbarrier of either CTA of the pair (a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar_cluster)
-      : "memory");
-}
-// The same over a 3-D map [E][rows][cols] (x = column, y = row, z = expert):
-// rows and columns past the expert's extent read the fill value (zero).
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
-      : "memory");
-}
-// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256.
-__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive once on the mbarrier at this offset in both CTAs when this thread's MMAs complete.
-__device__ __forceinline__ void tc_commit_pair_both(uint32_t bar) {
-  const uint16_t mask = 3;
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit_pair_local(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle, descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
 
 // Instruction descriptor for kind::f16: fp32 D, bf16 A and B, M rows (128, or 256 for a pair).
 template <int N, bool A_MN, bool B_MN, int M = BM>
@@ -381,30 +149,6 @@ __device__ __forceinline__ void tc_mma_pair_mx(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
       : "memory");
 }
-
-// Shared memory -> TMEM of both CTAs of the pair (each from its own shared
-// memory): a 32 x 128-bit block (512 B, rows 16 B apart) to lanes 0-31 of four
-// consecutive columns, repeated in the other three lane quarters.
-__device__ __forceinline__ void tc_cp_pair_32x128(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
-}
-
-// Shared-memory descriptor of an unswizzled block of 16-byte rows (8-row core
-// matrices 128 B apart), descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128u >> 4) << 16;
-  d |= static_cast<uint64_t>(128u >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d;
-}
-
-// silu(g) = g * sigmoid(g) with the fast exponential and reciprocal: a few
-// ulp of fp32, far below the bf16 rounding of H. For g < -87 the denominator
-// overflows and the quotient is 0, the limit of silu.
-__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 // nvalid: the row's columns left from dst (a multiple of 8); 8-column chunks
 // past it are not written.
@@ -550,19 +294,6 @@ __device__ __forceinline__ void pad_straddle_step(const int* s_off, const PadJob
 template <int KIND>
 __host__ __device__ constexpr uint32_t pair_epi_bytes() {
   return 4u * 2u * 4096u;
-}
-
-// Writes 32 consecutive columns (values v) of this lane's row into a
-// [32 rows x 64 bf16] box with 128-byte swizzle, at 16-byte chunk j0 .. j0+3.
-__device__ __forceinline__ void stage_row32(uint8_t* box, int lane, int j0, const float (&v)[32]) {
-#pragma unroll
-  for (int jj = 0; jj < 4; ++jj) {
-    const int off = lane * 128 + (((j0 + jj) ^ (lane & 7)) << 4);
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = v[8 * jj + i];
-    *reinterpret_cast<uint4*>(box + off) = pack8(f);
-  }
 }
 
 __device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const float (&v)[32], int nvalid) {
@@ -1230,11 +961,6 @@ __device__ __forceinline__ WTile decode_wgrad_pair(int t, int rank, const Params
   return tl;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
-}
-
 constexpr uint32_t kWgradPairEpiBytes = 4u * 2u * 4096u;
 constexpr int kWgradPairBars(int stages) { return 2 * stages + 5; }
 
@@ -1354,18 +1080,27 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
             // straddling k-block: A in 16-row boxes, the last one zero-padded; the
             // K16 steps past it are neither loaded nor read
             const int nfull = kvalid >> 4;
-            if (leader) mbar_expect_tx(fb, 2 * (static_cast<uint32_t>(nfull + 1) * 2 * 2048u + B_BYTES));
+            const uint32_t steps = static_cast<uint32_t>(nfull + 1) * 2 * 2048u;   // one operand's boxes
+            if (leader) mbar_expect_tx(fb, 2 * (steps + (p.pad_b ? steps : B_BYTES)));
 #pragma unroll
             for (int atom = 0; atom < 2; ++atom) {
               const uint32_t da = sa + atom * MN_ATOM;
               const int x = tl.m0 + 64 * atom;
               for (int kk = 0; kk < nfull; ++kk) tma_load_2d_pair(da + kk * 2048, &tmA16, fr, x, ky + 16 * kk);
               tma_load_2d_pair(da + nfull * 2048, &tmP, fr, x, tl.e * 16);
+              if (KIND == WGRAD_D && p.pad_b) {
+                const uint32_t db = sa + A_BYTES + atom * MN_ATOM;
+                const int xb = nb + 64 * atom;
+                for (int kk = 0; kk < nfull; ++kk) tma_load_2d_pair(db + kk * 2048, &tmB2, fr, xb, ky + 16 * kk);
+                tma_load_2d_pair(db + nfull * 2048, &tmC1, fr, xb, tl.e * 16);
+              }
             }
           }
-          const CUtensorMap* mb = tl.part ? &tmB2 : &tmB;   // dG or dU half (gate/up)
-          tma_load_2d_pair(sa + A_BYTES, mb, fr, nb, ky);
-          tma_load_2d_pair(sa + A_BYTES + MN_ATOM, mb, fr, nb + 64, ky);
+          if (!(KIND == WGRAD_D && p.pad_b && (kvalid & 15) != 0)) {
+            const CUtensorMap* mb = tl.part ? &tmB2 : &tmB;   // dG or dU half (gate/up)
+            tma_load_2d_pair(sa + A_BYTES, mb, fr, nb, ky);
+            tma_load_2d_pair(sa + A_BYTES + MN_ATOM, mb, fr, nb + 64, ky);
+          }
           fpar ^= 1u << stage;
           fused |= 1u << stage;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -1458,6 +1193,7 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
     for (int t = cid; t < total; t += ncl) {
       const WTile tl = decode_wgrad_pair<KIND>(t, static_cast<int>(rank), p, s_off);
       const bool empty = (tl.nkb == 0);   // expert without rows: its gradient is zero
+      if (empty && p.accumulate) continue;
       if (!empty) {
         if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status)) break;
         tc_fence_after();
@@ -1489,7 +1225,9 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
         __syncwarp();
         if (lane == 0) {
           // 3-D maps [E][rows][cols] of dW: rows and columns past the expert's are clipped
-          tma_store_3d(tl.part ? &tmC1 : &tmC0, smem_u32(stg), tl.n0 + c, mrow, tl.e);
+          const CUtensorMap* tmC = tl.part ? &tmC1 : &tmC0;
+          if (p.accumulate) tma_add_3d(tmC, smem_u32(stg), tl.n0 + c, mrow, tl.e);
+          else tma_store_3d(tmC, smem_u32(stg), tl.n0 + c, mrow, tl.e);
           bulk_commit();
         }
         // Spread the tile's stores over ~40% of the next tile's MMA time (~0.3 us of
@@ -1524,6 +1262,20 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
   }
 }
 
+// The zero-padded straddling steps of both operands (a CTA per expert and operand), for weight
+// gradients that no dH launch precedes.
+__global__ void __launch_bounds__(128)
+pad_steps_kernel(const int32_t* offsets, int M, const PadJob a, const PadJob b) {
+  __shared__ int s_off[2];
+  pdl_enter();
+  if (threadIdx.x < 2) s_off[threadIdx.x] = __ldg(offsets + blockIdx.x + threadIdx.x);
+  __syncthreads();
+  if (!index_ok(s_off[0] >= 0 && s_off[0] <= s_off[1] && s_off[1] <= M)) return;
+  const PadJob& j = blockIdx.y ? b : a;
+  pad_straddle_step(s_off, PadJob{j.a, j.pad + static_cast<size_t>(blockIdx.x) * 16 * j.C, j.C}, 0,
+                    threadIdx.x, 128);
+}
+
 // ----------------------------------------------------------------- diagnostics
 // One thread waits, through the GEMMs' bounded wait, on an mbarrier that nothing
 // arrives on; the wait runs out after timeout_ns and records the timeout.
@@ -1541,91 +1293,6 @@ __global__ void wait_timeout_kernel(int* status, uint64_t timeout_ns) {
 }
 
 // ----------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
-// 2-D tensor map over a row-major [outer, inner] array of bf16 (or fp32), 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
-              uint32_t box_outer, bool fp32 = false, uint64_t row_elems = 0) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {(row_elems ? row_elems : inner) * (fp32 ? 4 : 2)};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// One half of a row-major [rows, 2 * half] bf16 array ([G | U] and [dG | dU]):
-// columns [col0, col0 + half) of every row as a [rows, half] tensor, so a box
-// past column half reads zeros and a store past it is clipped (the other half
-// is never touched).
-bool make_half_map(CUtensorMap* m, const void* base, uint64_t half, uint64_t rows, uint64_t col0,
-                   uint32_t box_inner, uint32_t box_outer) {
-  return make_map(m, static_cast<const uint16_t*>(base) + col0, half, rows, box_inner, box_outer,
-                  false, 2 * half);
-}
-
-// 3-D tensor map over a row-major [E, rows, cols] array of bf16 (or fp32), 128-byte
-// swizzle: boxes of box_cols x box_rows x 1 at (column, row, expert); rows and
-// columns past an expert's extent read zeros and are clipped on stores.
-bool make_map3(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t E,
-               uint32_t box_cols, uint32_t box_rows, bool fp32 = false) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const uint64_t es_b = fp32 ? 4 : 2;
-  cuuint64_t dims[3] = {cols, rows, E};
-  cuuint64_t strides[2] = {cols * es_b, cols * rows * es_b};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D tensor map over a row-major [outer, inner] array of bytes (E4M3), 128-byte
-// swizzle unless another is given.
-bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-                 uint32_t box_inner, uint32_t box_outer,
-                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tensor map over n_atoms 512-byte scale atoms (as [n_atoms, 128] uint32), one atom per box.
-bool make_map_atoms(CUtensorMap* m, const void* base, uint64_t n_atoms) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {128, n_atoms};
-  cuuint64_t strides[1] = {512};
-  cuuint32_t box[2] = {128, 1};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 #ifndef MOE_PAIR_BN_MAX
 #define MOE_PAIR_BN_MAX 256
 #endif
@@ -1635,49 +1302,6 @@ constexpr size_t pair_smem_bytes(int E) {
   return 1024 + STAGES * (BM * BK * 2 + (BN / 2) * BK * 2 +
                           (FP8 ? ((512 * (1 + BN / 128) + 1023) & ~1023) : 0)) +
          pair_epi_bytes<KIND>() + 8 * (2 * STAGES + 11) + 16 + sizeof(int) * 2 * (E + 1) + 16;
-}
-
-// Launches a cluster-of-two kernel on as many clusters as can be resident
-// (at most tiles_upper). The shared-memory opt-in and the occupancy query run
-// once per kernel instantiation and device (the caller owns those two slots).
-template <typename... KArgs, typename... Args>
-int launch_cluster2(void (*kern)(KArgs...), size_t sm, size_t sm_max, int* configured,
-                    int* max_clusters, long long tiles_upper, const char* name, cudaStream_t st,
-                    const Args&... args) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = sm;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (*configured != dev) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(sm_max));
-    if (e != cudaSuccess) { set_last_cuda_error(e); return MOE_ERR_CUDA; }
-    cudaLaunchConfig_t q = cfg;
-    q.gridDim = dim3(2 * num_sms(), 1, 1);
-    q.dynamicSmemBytes = sm_max;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &q);
-    if (e != cudaSuccess || n < 1) {
-      set_last_cuda_error(e == cudaSuccess ? cudaErrorInvalidConfiguration : e);
-      return MOE_ERR_CUDA;
-    }
-    *max_clusters = n;
-    *configured = dev;
-  }
-  long long ncl = *max_clusters;
-  if (tiles_upper < ncl) ncl = tiles_upper;
-  if (ncl < 1) return MOE_OK;
-  ProfScope prof(name, st);
-  return launch_pdl(kern, static_cast<unsigned>(2 * ncl), kThreads, sm, st, 2, args...);
 }
 
 // Launches the CTA-pair kernel of a forward or input-gradient kind with the
@@ -1691,7 +1315,7 @@ int launch_pair(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& 
   static thread_local int max_clusters = 0;
   static const char* kNames[] = {"gemm_gate_up", "gemm_down", "gemm_dh", "gemm_dx", "", ""};
   static const char* kNamesFp8[] = {"gemm_gate_up_fp8", "gemm_down_fp8", "", "", "", ""};
-  return launch_cluster2(grouped_gemm_pair_kernel<KIND, BN, STAGES, FP8>,
+  return launch_cluster2(grouped_gemm_pair_kernel<KIND, BN, STAGES, FP8>, kThreads,
                          pair_smem_bytes<KIND, BN, STAGES, FP8>(p.E),
                          pair_smem_bytes<KIND, BN, STAGES, FP8>(e_max), &configured,
                          &max_clusters, tiles_upper, FP8 ? kNamesFp8[KIND] : kNames[KIND], st, a,
@@ -1716,7 +1340,7 @@ int launch_pair_wgrad_stages(const CUtensorMap& a, const CUtensorMap& b, const C
                              cudaStream_t st) {
   static thread_local int configured = -1;
   static thread_local int max_clusters = 0;
-  return launch_cluster2(grouped_gemm_pair_wgrad_kernel<KIND, STAGES>,
+  return launch_cluster2(grouped_gemm_pair_wgrad_kernel<KIND, STAGES>, kThreads,
                          pair_wgrad_smem_bytes<STAGES>(p.E),
                          pair_wgrad_smem_bytes<STAGES>(STAGES == 6 ? kWgradPair6MaxE : 1024),
                          &configured, &max_clusters, tiles,
@@ -1736,7 +1360,6 @@ int launch_pair_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
   return launch_pair_wgrad_stages<KIND, 5>(a, b, b2, c0, c1, a16, pad, p, tiles, st);
 }
 
-constexpr long long kSmemOptIn = 232448;   // shared memory a CTA may opt into
 
 // Largest expert count whose offset tables fit beside STAGES pair stages (-1: none).
 template <int KIND, int BN, int STAGES, bool FP8 = false>
@@ -1807,6 +1430,9 @@ inline int pair_bn(int n) {
 size_t ffn_backward_scratch(long long M, int E, int d, int I) {
   return (static_cast<size_t>(M) * 2 * I + static_cast<size_t>(E) * 16 * (d + I)) * sizeof(uint16_t);
 }
+
+// Padded straddling steps of X and dY for moe_grouped_gemm_wgrad: bf16 [E, 16, K], [E, 16, N].
+size_t wgrad_scratch(int E, int K, int N) { return static_cast<size_t>(E) * 16 * (K + N) * sizeof(uint16_t); }
 
 long long mxfp8_row_tiles(long long M, int E);                                     // fp8.cu
 int launch_quantize_rows(const void* x, const int32_t* offsets, int E, int M, int K, void* q,
@@ -2074,6 +1700,91 @@ extern "C" int moe_grouped_ffn_backward_weights(const moe_bf16* dy, const moe_bf
   return ffn_backward_parts(kBwdWeights, dy, xp, nullptr, h, offsets, E, M, d, I, nullptr,
                             nullptr, nullptr, nullptr, dw_gate, dw_up, dw_down, ws, ws_bytes,
                             stream);
+}
+
+// One product per expert: the down projection's kernel (W as [E][K][N]) or, transposed, the
+// input gradient's with one half (W as [E][N][K]).
+extern "C" int moe_grouped_gemm(const moe_bf16* x, const int32_t* offsets, int E, int M, int K,
+                                int N, const moe_bf16* w, int trans, moe_bf16* y, void* ws,
+                                size_t ws_bytes, void* stream) {
+  using namespace moe;
+  using namespace moe::gemm;
+  if (!ffn_shape_ok(E, M, K, N)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !offsets || !w || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(offsets) || !aligned16(w) || !aligned16(y)) return MOE_ERR_MISALIGNED;
+  if (!ws || ws_bytes < kWorkspaceHeader || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  if (cc_major() < 10) return MOE_ERR_UNSUPPORTED;
+  const int bn = pair_bn(N);
+  CUtensorMap ta, tb, tc;
+  if (!make_map(&ta, x, K, M, 64, BM) || !make_map(&tc, y, N, M, 64, 32) ||
+      !(trans ? make_map3(&tb, w, K, N, E, 64, bn / 2) : make_map3(&tb, w, N, K, E, 64, 64)))
+    return MOE_ERR_CUDA;
+  Params p{};
+  p.offsets = offsets;
+  p.E = E;
+  p.M = M;
+  p.n_tiles = (N + bn - 1) / bn;
+  p.k_blocks = p.kb_half = (K + BK - 1) / BK;
+  p.out = reinterpret_cast<__nv_bfloat16*>(y);
+  p.ld_out = N;
+  p.status = static_cast<int*>(ws);
+  const long long tiles = ((static_cast<long long>(M) + BM - 1) / BM + E) * p.n_tiles;
+  cudaStream_t st = as_stream(stream);
+  return trans ? launch_pair_bn<BWD_DX>(bn, ta, tb, tb, tc, tc, ta, tc, p, tiles, st)
+               : launch_pair_bn<FWD_DOWN>(bn, ta, tb, tb, tc, tc, tc, tc, p, tiles, st);
+}
+
+// dW[e] (+)= X_e^T dY_e: the padded straddling steps of X and dY, then the down projection's weight
+// gradient kernel, whose stores add to dW when accumulating (bulk tensor reductions; one per
+// element, so the result is the same on every run).
+extern "C" int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, const int32_t* offsets,
+                                      int E, int M, int K, int N, int accumulate, float* dw,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  using namespace moe::gemm;
+  if (!ffn_shape_ok(E, M, K, N)) return MOE_ERR_INVALID_ARG;
+  if (!offsets || !dw || (M > 0 && (!x || !dy))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(offsets) || !aligned16(dw)) return MOE_ERR_MISALIGNED;
+  if (!ws || !aligned16(ws) || ws_bytes < kWorkspaceHeader + wgrad_scratch(E, K, N)) return MOE_ERR_WORKSPACE;
+  if (cc_major() < 10) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t st = as_stream(stream);
+  if (M == 0) {
+    if (accumulate) return MOE_OK;
+    const cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * static_cast<size_t>(E) * K * N, st);
+    if (e != cudaSuccess) set_last_cuda_error(e);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  auto pad_x = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(ws) + kWorkspaceHeader);   // [E, 16, K]
+  auto pad_y = pad_x + static_cast<size_t>(E) * 16 * K;                                       // [E, 16, N]
+  {
+    ProfScope prof("gemm_pad_steps", st);
+    const int rc = launch_pdl(pad_steps_kernel, dim3(E, 2), 128, 0, st, 1, offsets, M,
+                              PadJob{reinterpret_cast<const __nv_bfloat16*>(x), pad_x, K},
+                              PadJob{reinterpret_cast<const __nv_bfloat16*>(dy), pad_y, N});
+    if (rc) return rc;
+  }
+  CUtensorMap ta, tb, tc, ta16, tb16, tpa, tpb;
+  if (!make_map(&ta, x, K, M, 64, 64) || !make_map(&tb, dy, N, M, 64, 64) ||
+      !make_map3(&tc, dw, N, K, E, 32, 32, true) || !make_map(&ta16, x, K, M, 64, 16) ||
+      !make_map(&tb16, dy, N, M, 64, 16) ||
+      !make_map(&tpa, pad_x, K, static_cast<uint64_t>(E) * 16, 64, 16) ||
+      !make_map(&tpb, pad_y, N, static_cast<uint64_t>(E) * 16, 64, 16))
+    return MOE_ERR_CUDA;
+  Params p{};
+  p.offsets = offsets;
+  p.E = E;
+  p.M = M;
+  p.d = N;
+  p.I = K;
+  p.m_tiles = (K + 2 * BM - 1) / (2 * BM);
+  p.n_tiles = (N + 255) / 256;
+  p.outf0 = dw;
+  p.accumulate = accumulate != 0;
+  p.pad_b = 1;
+  p.status = static_cast<int*>(ws);
+  return launch_pair_wgrad<WGRAD_D>(ta, tb, tb16, tc, tpb, ta16, tpa, p,
+                                    static_cast<long long>(E) * p.m_tiles * p.n_tiles, st);
 }
 
 extern "C" int moe_debug_wait_timeout(void* ws, int timeout_us, void* stream) {

@@ -74,7 +74,9 @@ enum moe_op {
   MOE_OP_GROUPED_FFN_FP8 = 7,
   MOE_OP_ROUTE_PERMUTE_EP = 8,
   MOE_OP_NORM_BACKWARD = 9,
-  MOE_OP_GROUPED_FFN_W4 = 10
+  MOE_OP_GROUPED_FFN_W4 = 10,
+  MOE_OP_GROUPED_FFN_FP4 = 11,
+  MOE_OP_GROUPED_GEMM_WGRAD = 12
 };
 
 /* Bytes of device workspace the operation needs for these sizes (0 on bad
@@ -651,6 +653,112 @@ int moe_grouped_ffn_w4(const moe_bf16* x, const int32_t* perm, int T, int K,
                        int group_d, const uint8_t* wgu, const moe_bf16* wgu_s, const uint8_t* wd,
                        const moe_bf16* wd_s, moe_bf16* y, moe_bf16* h, void* ws, size_t ws_bytes,
                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products grouped by expert, by themselves: for experts that are not SwiGLU
+ * ([MOD]'s are not gated), for adapters beside them, for any matrix per segment.
+ * ------------------------------------------------------------------------ */
+
+/* y[p] = bf16(x[p] W[e]) for expert e's rows [offsets[e], offsets[e+1]), fp32 accumulation.
+ *   x [M,K] bf16 in; offsets [E+1] int32 as in moe_grouped_ffn.
+ *   trans == 0: w [E,K,N] bf16.  trans != 0: w [E,N,K] bf16, y = x W[e]^T (the input
+ *   gradient of the product with trans == 0: dx = dy W[e]^T, K and N exchanged).
+ *   y [M,N] bf16 out; rows past offsets[E] are not written.
+ *   ws: a workspace header (256 bytes). K % 8 == 0, N % 8 == 0, E <= 1024. */
+int moe_grouped_gemm(const moe_bf16* x, const int32_t* offsets, int E, int M, int K, int N,
+                     const moe_bf16* w, int trans, moe_bf16* y, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Its weight gradient: dw[e] = x_e^T dy_e (fp32), or dw[e] += with accumulate != 0 (the
+ * sum of one call is added once to each element, so results are the same bits on every run).
+ *   x [M,K], dy [M,N] bf16 in; dw [E,K,N] fp32. Experts without rows: zero, or unchanged.
+ *   An expert's dw depends on its own rows alone (an Inf or NaN in others' stays there).
+ *   ws: moe_workspace_size(MOE_OP_GROUPED_GEMM_WGRAD, M, E, 1, 1, K, N) bytes. */
+int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, const int32_t* offsets, int E,
+                           int M, int K, int N, int accumulate, float* dw, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floats. Elements are E2M1 (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their
+ * negatives), two to a byte along K, the even one in the low half. With block 16 every 16
+ * elements share an E4M3 scale s, and a row (activations) or an expert's matrix (weights) a
+ * 32-bit factor g: an element stands for q s g. With block 32 every 32 share a power of two
+ * 2^X, kept as the byte X + 127, and there is no factor. All rounding is to nearest, ties to
+ * the even code. Activations and weights of one product have the same block.
+ *
+ * Quantizing v (block 16): g = 2^n, n >= -100 the smallest with max|v| <= 2688 g over the
+ *   row (or matrix); s = E4M3(max|v| / (6 g)) over the block; q = E2M1(v / (s g)), 0 where
+ *   s is 0. A row with an Inf or NaN keeps g = NaN, and everything computed from it is NaN.
+ * Quantizing v (block 32): X = floor(log2 max|v|) - 2 within [-126, 125] (-126 for zeros);
+ *   q = E2M1(v 2^-X), at most 6 in size. A block with an Inf or NaN keeps the byte 255 (NaN).
+ *
+ * Scales for the tensor cores are 512-byte atoms of 128 rows x 4 scales, a row's four in one
+ * 32-bit word, words ordered (row % 32) * 4 + row / 32; KA = ceil(K / (4 block)) atoms follow one another along
+ * K. Row tiles of activations follow the experts: the rows of expert e fill tiles from 2 P(e)
+ * on, P(e) = sum over earlier experts of ceil(ceil(n / 128) / 2); (ceil(M / 128) + 2E) tiles
+ * hold any split. K % 64 == 0 throughout.
+ * ------------------------------------------------------------------------ */
+
+/* moe_dispatch_scatter into 4-bit rows: token t's row quantized once and written to row
+ * inv_perm[t*K + j] for each j < K (inv_perm NULL, K == 1: row t; x is in expert order).
+ *   x [T,d] bf16, inv_perm [T*K] int32, offsets [E+1] int32 in.
+ *   q [T*K, d/2] uint8, sf [tiles, KA, 512] uint8 (tiles for M = T*K), row_scale [T*K] fp32
+ *   (block 16; NULL with block 32) out. Scales of rows past an expert's last row are not
+ *   written. 64 <= d <= 16384, K <= 32, E <= 1024. */
+int moe_fp4_quantize_rows(const moe_bf16* x, const int32_t* inv_perm, int T, int K,
+                          const int32_t* offsets, int E, int d, int block, uint8_t* q, uint8_t* sf,
+                          float* row_scale, void* stream);
+
+/* The rows back in bf16: out [M,d] (rows past offsets[E] are not written). */
+int moe_fp4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const float* row_scale,
+                            const int32_t* offsets, int E, int M, int d, int block, moe_bf16* out,
+                            void* stream);
+
+/* Weights w [E,K,N] bf16 (N contiguous, as moe_grouped_ffn takes them) as a plain 4-bit
+ * checkpoint, K contiguous: codes [E,N,K/2] uint8, scales [E,N,K/block] uint8, scale [E]
+ * fp32 (block 16; NULL with block 32). N % 8 == 0, E <= 65535. */
+int moe_fp4_quantize_weights(const moe_bf16* w, int E, int K, int N, int block, uint8_t* codes,
+                             uint8_t* scales, float* scale, void* stream);
+
+/* The block scales of a plain checkpoint as atoms (once, when weights are loaded; the codes
+ * stay as they are).
+ *   scales_b NULL: sf [E, ceil(N/128), KA, 512], tile i holding rows 128 i ...
+ *   scales_a the gate's and scales_b the up projection's (N = I, N % 64 == 0): sf
+ *   [E, N/64, KA, 512]; with I % 128 == 0 tiles alternate 128 rows of gate and 128 of up,
+ *   otherwise a tile holds 64 rows of gate, then 64 of up. */
+int moe_fp4_pack_scales(const uint8_t* scales_a, const uint8_t* scales_b, int E, int N, int K,
+                        int block, uint8_t* sf, void* stream);
+
+/* y[p] = bf16(row_scale[p] w_scale[e] * sum_k (q s)_x (q s)_w) for expert e's rows, products
+ * exact, fp32 accumulation.
+ *   xq, xsf, row_scale from moe_fp4_quantize_rows (M rows of K); w [E,N,K/2] codes, w_sf from
+ *   moe_fp4_pack_scales, w_scale [E]; with block 32 row_scale and w_scale are not read.
+ *   y [M,N] bf16 out; rows past offsets[E] are not written.
+ *   ws: a workspace header (256 bytes). N % 8 == 0, E <= 1024. */
+int moe_grouped_gemm_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row_scale,
+                         const int32_t* offsets, int E, int M, int K, int N, int block,
+                         const uint8_t* w, const uint8_t* w_sf, const float* w_scale, moe_bf16* y,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Grouped SwiGLU experts on 4-bit activations and weights, forward: G, U the products with
+ * w_gate and w_up, H = silu(G) U, y = bf16(quantized H times w_down). H is quantized
+ *   block 16, h_scale [E] fp32 given: with g = h_scale[e] (> 0, from a calibration run: about
+ *     its largest |H| / 2688), larger values saturating at 2688 h_scale[e]; fp32 H, one pass;
+ *   block 16, h_scale NULL: H rounded to bf16, then as moe_fp4_quantize_rows does (its rows
+ *     scaled by their own maximum; one more pass over H);
+ *   block 32: as rows of block 32 are, from fp32 H (h_scale must be NULL).
+ *   A block of H with an Inf or NaN makes its row of y NaN.
+ *   w_gate, w_up [E,I,d/2], wgu_sf their scales packed together, gate_scale, up_scale [E];
+ *   w_down [E,d,I/2], wd_sf, down_scale [E] (factors not read with block 32).
+ *   y [M,d] bf16 out; rows past offsets[E] are not written.
+ *   ws: moe_workspace_size(MOE_OP_GROUPED_FFN_FP4, M, E, 1, 1, d, I) bytes.
+ * d % 64 == 0, I % 64 == 0, I <= 16384, E <= 1024. */
+int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row_scale,
+                        const int32_t* offsets, int E, int M, int d, int I, int block,
+                        const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* wgu_sf,
+                        const float* gate_scale, const float* up_scale, const uint8_t* w_down,
+                        const uint8_t* wd_sf, const float* down_scale, const float* h_scale,
+                        moe_bf16* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Diagnostics: runs the bounded device-side wait that every mbarrier wait of
  * the GEMM kernels uses, on an mbarrier that nothing completes, with a limit of
