@@ -232,7 +232,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued[STAGES];
@@ -285,85 +285,68 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (leader) {
+    if (leader && elect_one()) {
       const int my_tiles = total > cid ? (total - cid + ncl - 1) / ncl : 0;
-      const long long blocks = static_cast<long long>(my_tiles) * k_blocks;
-      // Block n of this cluster's k-blocks: its stage's full barrier, then a scale slot whose
-      // last readers (block n - kRing) have completed, then the copies.
-      int cp_stage = 0, cp_slot = 0, old_stage = 0;
-      uint32_t cp_phase = 0, old_phase = 0;
-      long long copied = 0;
-      auto copy_scales = [&]() -> bool {
-        if (!mbar_wait(full_bar(cp_stage), cp_phase, abort_flag, p.status)) return false;
-        if (copied >= kRing) {
-          if (!mbar_wait(empty_bar(old_stage), old_phase, abort_flag, p.status)) return false;
-          if (++old_stage == STAGES) { old_stage = 0; old_phase ^= 1u; }
-        }
+      // descriptors of stage 0; other addresses are added in units of 16 bytes
+      const uint64_t desc_op = smem_desc(smem_base, 16, 1024);
+      const uint64_t desc_sf = smem_desc_rows16(smem_base + S::A + S::B);
+      int stage = 0, slot_i = 0, old_stage = 0;
+      uint32_t phase = 0, old_phase = 0;
+      int fresh = kRing;   // scale slots not yet used
+      bool ok = true;
+      for (int j = 0; j < my_tiles && ok; ++j) {
+        if (!mbar_wait(tempty_bar, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t slot = tmem_base + kScaleCol + S::SLOT * static_cast<uint32_t>(cp_slot);
-          const uint32_t ssa = smem_base + cp_stage * S::STAGE + S::A + S::B;
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) { ok = false; break; }
+          // the slot's last readers, the MMAs of kRing blocks ago, have completed
+          if (fresh) {
+            --fresh;
+          } else {
+            if (!mbar_wait(empty_bar(old_stage), old_phase, abort_flag, p.status)) { ok = false; break; }
+            if (++old_stage == STAGES) { old_stage = 0; old_phase ^= 1u; }
+          }
+          tc_fence_after();
+          const uint32_t slot = tmem_base + kScaleCol + S::SLOT * static_cast<uint32_t>(slot_i);
+          const uint64_t sf = desc_sf + static_cast<uint32_t>(stage) * (S::STAGE / 16);
 #pragma unroll
-          for (uint32_t k = 0; k < S::KA; ++k)
-            tc_cp_pair_32x128(slot + 4 * k, smem_desc_rows16(ssa + 512 * k));
+          for (uint32_t k = 0; k < S::KA; ++k) tc_cp_pair_32x128(slot + 4 * k, sf + 32 * k);
 #pragma unroll
           for (uint32_t j = 0; j < S::NB; ++j)
 #pragma unroll
             for (uint32_t k = 0; k < S::KA; ++k)
               tc_cp_pair_32x128(slot + 4 * S::KA + 4 * (k * S::NB + j),
-                                smem_desc_rows16(ssa + S::SA + 512 * (j * S::KA + k)));
-        }
-        __syncwarp();
-        if (++cp_stage == STAGES) { cp_stage = 0; cp_phase ^= 1u; }
-        if (++cp_slot == kRing) cp_slot = 0;
-        ++copied;
-        return true;
-      };
-      int stage = 0, slot_i = 0;
-      bool ok = true;
-      long long n = 0;
-      for (int j = 0; j < my_tiles && ok; ++j) {
-        if (!mbar_wait(tempty_bar, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        tc_fence_after();
-        for (int kb = 0; kb < k_blocks; ++kb, ++n) {
-          if (copied == n && !copy_scales()) { ok = false; break; }
-          // the next block's scales before this block's MMAs, if its operands have landed
-          if (n + 1 < blocks && copied == n + 1 && mbar_try(full_bar(cp_stage), cp_phase) &&
-              !copy_scales()) { ok = false; break; }
-          if (lane == 0) {
-            const uint32_t sa = smem_base + stage * S::STAGE;
-            const uint32_t sb = sa + S::A;
-            const uint32_t slot = tmem_base + kScaleCol + S::SLOT * static_cast<uint32_t>(slot_i);
-            const int steps = min(4, p.k64 - 4 * kb);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {   // K64 steps of 32 bytes
-              if (kk < steps) {
-                const uint32_t ka = BLOCK == 16 ? kk : kk / 2;
-                const uint32_t id = BLOCK == 16 ? 0u : 2u * (kk & 1);
-                mma_fp4<BLOCK>(tmem_base, smem_desc(sa + kk * 32, 16, 1024),
-                               smem_desc(sb + kk * 32, 16, 1024), IDESC | (id << 4) | (id << 29),
-                               slot + 4 * ka, slot + 4 * S::KA + 4 * S::NB * ka,
-                               (kb | kk) != 0 ? 1u : 0u);
-              }
-            }
-            tc_commit_pair_both(empty_bar(stage));
+                                sf + S::SA / 16 + 32 * (j * S::KA + k));
+          const uint64_t da = desc_op + static_cast<uint32_t>(stage) * (S::STAGE / 16);
+          const int steps = min(4, p.k64 - 4 * kb);
+          auto step = [&](uint32_t kk, uint32_t acc) {   // 64 K: 32 bytes of a row
+            const uint32_t ka = BLOCK == 16 ? kk : kk / 2;
+            const uint32_t id = BLOCK == 16 ? 0u : 2u * (kk & 1);
+            mma_fp4<BLOCK>(tmem_base, da + 2 * kk, da + S::A / 16 + 2 * kk,
+                           IDESC | (id << 4) | (id << 29), slot + 4 * ka,
+                           slot + 4 * S::KA + 4 * S::NB * ka, acc);
+          };
+          if (steps == 4) {
+            step(0, kb != 0);
+            step(1, 1);
+            step(2, 1);
+            step(3, 1);
+          } else {
+            for (int kk = 0; kk < steps; ++kk) step(kk, (kb | kk) != 0);
           }
-          __syncwarp();
-          if (++stage == STAGES) stage = 0;
+          tc_commit_pair_both(empty_bar(stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           if (++slot_i == kRing) slot_i = 0;
         }
         if (!ok) break;
-        if (lane == 0) tc_commit_pair_both(tfull_bar);
-        __syncwarp();
+        tc_commit_pair_both(tfull_bar);
       }
-      if (lane == 0) {
-        tc_commit_pair_local(drain_bar);
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kTimeoutNs) {
-        }
+      tc_commit_pair_local(drain_bar);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kTimeoutNs) {
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     // Two warps per 32 rows, each half the columns (SwiGLU: half of gate's and of up's).
@@ -399,7 +382,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(tempty_bar, 0));
+      // relaxed: the barrier orders TMEM reads alone, which have completed; a release would wait
+      // for the last tile's stores
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(tempty_bar, 0));
 
       if constexpr (EPI == OUT) {
         const float f = rs * f0 * f1;
@@ -550,10 +535,13 @@ struct Operands {
   int K;
 };
 
-constexpr int kStages = 4;
+// Stages beside the output staging, or without it.
+template <int EPI>
+constexpr int stages_of() { return EPI == OUT ? 4 : 5; }
 
 template <int EPI, int BLOCK, int BN>
 int launch_pair(const Operands& o, Params p, cudaStream_t st) {
+  constexpr int kStages = stages_of<EPI>();
   using S = Shape<EPI, BLOCK, BN, kStages>;
   static_assert(S::smem(1024) <= kSmemOptIn, "shared memory");
   static thread_local int configured = -1;

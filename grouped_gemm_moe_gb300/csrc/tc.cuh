@@ -170,6 +170,15 @@ __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp. A branch on it is uniform to the compiler, which a branch on
+// the lane number is not: tcgen05 instructions take their operands from uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
+
 // ---- CTA-pair (cluster of two, tcgen05 cta_group::2) helpers
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
