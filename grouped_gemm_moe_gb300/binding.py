@@ -1133,23 +1133,27 @@ def _fp4_atoms(K: int, block: int) -> int:
 
 
 def _fp4_rows_shapes(M: int, d: int, E: int, block: int):
-    tiles = -(-M // 128) + 2 * E
-    return (M, d // 2), (tiles, _fp4_atoms(d, block), 512), (M,)
+    return (M, d // 2), (-(-M // 128) + 2 * E, _fp4_atoms(d, block), 512), (M,)
+
+
+def _given(t, dtype, shape, name: str, dev):
+    """_shaped for a tensor that has to be there."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    _shaped(t, dtype, shape, name, dev)
 
 
 def _fp4_rows(rows, E: int, block: int, dev):
     """(q, sf, row_scale, M, K) of checked rows from moe_fp4_quantize_rows."""
     q, sf, rs = rows
     _need(q, torch.uint8, 2, "q")
-    M, d = q.shape[0], 2 * q.shape[1]
+    M, half = q.shape
+    d = 2 * half
     _fp4_block(block, d, "K")
     _, s_sf, s_rs = _fp4_rows_shapes(M, d, E, block)
-    _shaped(q, torch.uint8, (M, d // 2), "q", dev)
-    _need(sf, torch.uint8, 3, "sf")
-    _shaped(sf, torch.uint8, s_sf, "sf", dev)
+    _given(sf, torch.uint8, s_sf, "sf", dev)
     if block == 16:
-        _need(rs, torch.float32, 1, "row_scale")
-        _shaped(rs, torch.float32, s_rs, "row_scale", dev)
+        _given(rs, torch.float32, s_rs, "row_scale", dev)
     else:
         rs = None
     return q, sf, rs, M, d
@@ -1243,8 +1247,7 @@ def moe_fp4_pack_scales(scales_a: torch.Tensor, scales_b: Optional[torch.Tensor]
 def _fp4_factor(t: Optional[torch.Tensor], E: int, block: int, name: str, dev):
     if block == 32:
         return None
-    _need(t, torch.float32, 1, name)
-    _shaped(t, torch.float32, (E,), name, dev)
+    _given(t, torch.float32, (E,), name, dev)
     return t
 
 
@@ -1259,7 +1262,7 @@ def moe_grouped_gemm_fp4(rows, offsets: torch.Tensor, w, block: int = 16,
     _need(codes, torch.uint8, 3, "codes")
     N = codes.shape[1]
     _shaped(codes, torch.uint8, (E, N, K // 2), "codes", dev)
-    _shaped(wsf, torch.uint8, (E, -(-N // 128), _fp4_atoms(K, block), 512), "weight scales", dev)
+    _given(wsf, torch.uint8, (E, -(-N // 128), _fp4_atoms(K, block), 512), "weight scales", dev)
     scale = _fp4_factor(scale, E, block, "scale", dev)
     ws = _need_ws(ws, WORKSPACE_HEADER, dev)
     if out is None:
@@ -1288,14 +1291,10 @@ def moe_grouped_ffn_fp4(rows, offsets: torch.Tensor, wgu, wd, block: int = 16,
     if I % 64 or I < 64:
         raise ValueError(f"I must be a multiple of 64, got {I}")
     _shaped(gate, torch.uint8, (E, I, d // 2), "gate codes", dev)
-    _need(up, torch.uint8, 3, "up codes")
-    _shaped(up, torch.uint8, (E, I, d // 2), "up codes", dev)
-    _need(gsf, torch.uint8, 4, "gate and up scales")
-    _shaped(gsf, torch.uint8, (E, I // 64, _fp4_atoms(d, block), 512), "gate and up scales", dev)
-    _need(down, torch.uint8, 3, "down codes")
-    _shaped(down, torch.uint8, (E, d, I // 2), "down codes", dev)
-    _need(dsf, torch.uint8, 4, "down scales")
-    _shaped(dsf, torch.uint8, (E, -(-d // 128), _fp4_atoms(I, block), 512), "down scales", dev)
+    _given(up, torch.uint8, (E, I, d // 2), "up codes", dev)
+    _given(gsf, torch.uint8, (E, I // 64, _fp4_atoms(d, block), 512), "gate and up scales", dev)
+    _given(down, torch.uint8, (E, d, I // 2), "down codes", dev)
+    _given(dsf, torch.uint8, (E, -(-d // 128), _fp4_atoms(I, block), 512), "down scales", dev)
     gscale, uscale, dscale = (_fp4_factor(t, E, block, n, dev) for t, n in
                               ((gscale, "gate scale"), (uscale, "up scale"), (dscale, "down scale")))
     if h_scale is not None:

@@ -44,18 +44,168 @@ __device__ __forceinline__ int2 place_of(int p, const int* s_off, const int* s_t
   return p < s_off[E] ? make_int2(s_tile[lo] + local / 128, local & 127) : make_int2(-1, 0);
 }
 
-// Largest |bf16| of a word's two, as bits (Inf 0x7f80, NaN above it), kept in the upper half.
-__device__ __forceinline__ uint32_t top_bits(uint32_t m, uint32_t w) {
-  const uint32_t a = w & 0x7fff0000u, b = (w & 0x00007fffu) << 16;
-  return max(m, max(a, b));
+// Running maximum of |bf16| bits (Inf 0x7f80, NaN above it) of a word's two halves, each in its
+// own half, and the larger of the two as the bits of a float.
+__device__ __forceinline__ uint32_t top2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t top_of(uint32_t m) { return max(m & 0xffff0000u, m << 16); }
+
+// 32 bytes: one access where the address allows it (half as many requests), else two.
+__device__ __forceinline__ void load32(const uint4* src, bool wide, uint4& a, uint4& b) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(src));
+  } else {
+    a = ldg_nc_v4(src);
+    b = ldg_nc_v4(src + 1);
+  }
+}
+__device__ __forceinline__ void store32(uint4* dst, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ bool aligned32(const void* p) {   // rows are whole multiples of 128 bytes
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
 }
 
-// One launch quantizes each token's row once and writes it to its K rows in expert order
-// (inv_perm null: to its own row). HBM-bound: 2 bytes read and K (1/2 + 1/block) written an
-// element. TPR threads take a row (kThreads / TPR rows to a CTA), each BPT units of 16
-// elements held in registers between the row's maximum and the codes; consecutive threads
-// take consecutive units, so loads are 32 and stores 8 bytes a thread without gaps, and the
-// four units of a scale word meet by shuffles.
+// The largest |v| bits of a unit of 16 elements.
+__device__ __forceinline__ uint32_t unit_top(const uint4& a, const uint4& b) {
+  const uint32_t m = top2(top2(top2(top2(0u, a.x), a.y), a.z), a.w);
+  return top_of(top2(top2(top2(top2(m, b.x), b.y), b.z), b.w));
+}
+
+// Codes of a unit and, in the first lane of each scale word's units, the word: four
+// consecutive units' scales (block 16) or eight's (block 32, two units to a scale; past the
+// row's end threads without a unit give the byte of zeros). g, sixth: the row's factor and
+// fl(1/6) / g, fine: the row is finite (block 16). Every lane of the warp calls it.
+template <int BLOCK>
+__device__ __forceinline__ uint2 encode_unit(const uint4& a, const uint4& b, uint32_t top, float g,
+                                             float sixth, bool fine, uint32_t* word) {
+  float_pair v[8];
+  unpack8(a, v);
+  unpack8(b, v + 4);
+  uint32_t byte;
+  uint2 code;
+  if constexpr (BLOCK == 16) {
+    byte = fine ? scale_byte(__uint_as_float(top), sixth) : 0u;
+    code = fine ? codes16(v, byte, g) : make_uint2(0u, 0u);
+  } else {
+    const uint32_t both = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const bool ok = both < 0x7f800000u;
+    const int X = block_exponent(__uint_as_float(ok ? both : 0u));
+    byte = ok ? static_cast<uint32_t>(X + 127) : kNanE8m0;
+    code = ok ? codes32(v, X) : make_uint2(0u, 0u);
+  }
+  constexpr int kStep = BLOCK / 16;
+  const uint32_t b1 = __shfl_down_sync(0xffffffffu, byte, kStep);
+  const uint32_t b2 = __shfl_down_sync(0xffffffffu, byte, 2 * kStep);
+  const uint32_t b3 = __shfl_down_sync(0xffffffffu, byte, 3 * kStep);
+  *word = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
+  return code;
+}
+
+// Each token's row is quantized once and written to its K rows in expert order (inv_perm
+// null: to its own row). HBM-bound: 2 bytes read and K (1/2 + 1/block) written an element.
+// Rows of up to 192 units: a warp a row, its elements in registers between the row's maximum
+// and the codes (lane l takes units l, l + 32, ...: 32 bytes in, 8 bytes out, without gaps), no
+// barrier between rows; warps stay for many rows, so that the expert table is made once a
+// CTA. The lanes look the K destinations up side by side, and the scale words, each in a
+// sector of its own, are spread over the lanes before they are stored. Those words are what
+// keeps wide copies from HBM speed: 32768 x 4096 to 8 experts takes 191 us (floor 129), 134
+// without them. Block 16, rows of 2112 to 6: 27 us, a CTA of 128 threads a row 32; rows of 1408
+// to one: 77 us, 64 threads a row 93; rows of 4096 to 8: 220 us, 128 threads a row 191.
+template <int BLOCK, int BPT>
+__global__ void __launch_bounds__(kThreads)
+quantize_warp_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ inv_perm,
+                          const int32_t* __restrict__ offsets, int E, int T, int K, int M, int d,
+                          uint2* __restrict__ q, uint32_t* __restrict__ sf,
+                          float* __restrict__ row_scale) {
+  extern __shared__ int sm[];
+  int* s_off = sm;              // [E + 1]
+  int* s_tile = s_off + E + 1;  // [E + 1]
+  pdl_enter();
+  for (int e = threadIdx.x; e <= E; e += kThreads) s_off[e] = __ldg(offsets + e);
+  __syncthreads();
+  if (threadIdx.x < 32) tile_prefix(s_off, s_tile, E);
+  __syncthreads();
+  constexpr int kPer = BLOCK / 4;              // units of a scale word
+  constexpr int kWords = 32 / kPer;            // words of 32 units
+  constexpr int kHeld = (BPT * kWords + 31) / 32;
+  const bool wide = aligned32(x);
+  const int lane = threadIdx.x & 31;
+  const int units = d / 16;
+  const int ka = (units + kPer - 1) / kPer;
+  const unsigned warps = gridDim.x * (kThreads / 32);
+  for (unsigned t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < static_cast<unsigned>(T);
+       t += warps) {
+    uint4 a[BPT], b[BPT];
+    const uint4* src = x + static_cast<size_t>(t) * units * 2;
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) {
+      const int u = i * 32 + lane;
+      a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (u < units) {
+        load32(src + 2 * u, wide, a[i], b[i]);
+      }
+    }
+    int p = -1;
+    int2 pl = make_int2(-1, 0);
+    if (lane < K) {
+      p = inv_perm ? __ldg(inv_perm + static_cast<size_t>(t) * K + lane) : static_cast<int>(t);
+      if (!index_ok(p >= 0 && p < M)) p = -1;
+      if (p >= 0) pl = place_of(p, s_off, s_tile, E);
+    }
+    uint32_t top[BPT], row_top = 0;
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) {
+      top[i] = unit_top(a[i], b[i]);
+      row_top = max(row_top, top[i]);
+    }
+    float g = 1.f, sixth = kSixth;
+    bool fine = true;
+    if constexpr (BLOCK == 16) {
+      row_top = __reduce_max_sync(0xffffffffu, row_top);
+      fine = row_top < 0x7f800000u;
+      const int n = row_exponent(__uint_as_float(fine ? row_top : 0u));
+      g = two_to(n);
+      sixth = kSixth * two_to(-n);
+      if (p >= 0) row_scale[p] = fine ? g : __uint_as_float(0x7fc00000u);
+    }
+    uint2 code[BPT];
+    uint32_t held[kHeld];   // lane l: words l, l + 32, ...
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) {
+      uint32_t word;
+      code[i] = encode_unit<BLOCK>(a[i], b[i], top[i], g, sixth, fine, &word);
+      const uint32_t w = __shfl_sync(0xffffffffu, word, (lane % kWords) * kPer);
+      if ((i * kWords) % 32 == 0 || lane / kWords == (i * kWords) % 32 / kWords)
+        held[i * kWords / 32] = w;
+    }
+    for (int j = 0; j < K; ++j) {
+      const int pj = __shfl_sync(0xffffffffu, p, j);
+      const int tile = __shfl_sync(0xffffffffu, pl.x, j), row = __shfl_sync(0xffffffffu, pl.y, j);
+      if (pj < 0) continue;
+      uint2* dst = q + static_cast<size_t>(pj) * units;
+#pragma unroll
+      for (int i = 0; i < BPT; ++i)
+        if (i * 32 + lane < units) dst[i * 32 + lane] = code[i];
+      if (tile >= 0) {
+        uint32_t* ds = sf + static_cast<size_t>(tile) * ka * 128 + atom_word(row);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+          if (i * 32 + lane < ka) ds[static_cast<size_t>(i * 32 + lane) * 128] = held[i];
+      }
+    }
+  }
+}
+
+// Wider rows: TPR threads a row, BPT units each, the maximum joined in shared memory.
 template <int BLOCK, int TPR, int BPT>
 __global__ void __launch_bounds__(kThreads)
 quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ inv_perm,
@@ -71,6 +221,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
   pdl_enter();
   const int units = d / 16;
   const int sub = threadIdx.x / TPR, lane_r = threadIdx.x % TPR;
+  const bool wide = aligned32(x);
   const unsigned t = blockIdx.x * kRows + sub;
   const bool live = t < static_cast<unsigned>(T);
   uint4 a[BPT], b[BPT];
@@ -80,8 +231,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
     a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
     if (live && u < units) {
       const uint4* src = x + (static_cast<size_t>(t) * units + u) * 2;
-      a[i] = ldg_nc_v4(src);
-      b[i] = ldg_nc_v4(src + 1);
+      load32(src, wide, a[i], b[i]);
     }
   }
   for (int e = threadIdx.x; e <= E; e += kThreads) s_off[e] = __ldg(offsets + e);
@@ -92,10 +242,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
   uint32_t row_top = 0;
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
-    uint32_t m = top_bits(top_bits(0u, a[i].x), a[i].y);
-    m = top_bits(top_bits(m, a[i].z), a[i].w);
-    m = top_bits(top_bits(m, b[i].x), b[i].y);
-    top[i] = top_bits(top_bits(m, b[i].z), b[i].w);
+    top[i] = unit_top(a[i], b[i]);
     row_top = max(row_top, top[i]);
   }
   if constexpr (BLOCK == 16) {
@@ -115,43 +262,21 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
     s_pos[r][slot] = p;
     s_place[r][slot] = p >= 0 ? place_of(p, s_off, s_tile, E) : make_int2(-1, 0);
   }
-  int n = 0;
+  float g = 1.f, sixth = kSixth;
   bool fine = true;
   if constexpr (BLOCK == 16) {
 #pragma unroll
     for (int w = 0; w < TPR / 32; ++w) row_top = max(row_top, s_top[sub * (TPR / 32) + w]);
     fine = row_top < 0x7f800000u;
-    n = row_exponent(__uint_as_float(fine ? row_top : 0u));
+    const int n = row_exponent(__uint_as_float(fine ? row_top : 0u));
+    g = two_to(n);
+    sixth = kSixth * two_to(-n);
   }
   __syncthreads();
   uint2 code[BPT];
   uint32_t word[BPT];
 #pragma unroll
-  for (int i = 0; i < BPT; ++i) {
-    float_pair v[8];
-    unpack8(a[i], v);
-    unpack8(b[i], v + 4);
-    uint32_t byte;
-    if constexpr (BLOCK == 16) {
-      byte = fine ? to_e4m3(__fdiv_rn(__uint_as_float(top[i]), 6.f * two_to(n))) : 0u;
-      code[i] = fine ? codes16(v, byte, n) : make_uint2(0u, 0u);
-      const uint32_t b1 = __shfl_down_sync(0xffffffffu, byte, 1);
-      const uint32_t b2 = __shfl_down_sync(0xffffffffu, byte, 2);
-      const uint32_t b3 = __shfl_down_sync(0xffffffffu, byte, 3);
-      word[i] = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
-    } else {
-      const uint32_t both = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      const bool ok = both < 0x7f800000u;
-      const int X = block_exponent(__uint_as_float(ok ? both : 0u));
-      byte = ok ? static_cast<uint32_t>(X + 127) : kNanE8m0;
-      code[i] = ok ? codes32(v, X) : make_uint2(0u, 0u);
-      const uint32_t b1 = __shfl_down_sync(0xffffffffu, byte, 2);
-      const uint32_t b2 = __shfl_down_sync(0xffffffffu, byte, 4);
-      const uint32_t b3 = __shfl_down_sync(0xffffffffu, byte, 6);
-      // past the row's end (half an atom): threads without a unit give the byte of zeros
-      word[i] = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
-    }
-  }
+  for (int i = 0; i < BPT; ++i) code[i] = encode_unit<BLOCK>(a[i], b[i], top[i], g, sixth, fine, &word[i]);
   constexpr int kPer = BLOCK / 4;   // units of a scale word
   const int ka = (units + kPer - 1) / kPer;
   for (int j = 0; j < K; ++j) {
@@ -167,16 +292,17 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
         sf[(static_cast<size_t>(pl.x) * ka + u / kPer) * 128 + atom_word(pl.y)] = word[i];
     }
     if (BLOCK == 16 && lane_r == 0)
-      row_scale[p] = fine ? two_to(n) : __uint_as_float(0x7fc00000u);
+      row_scale[p] = fine ? g : __uint_as_float(0x7fc00000u);
   }
 }
 
-// Rows back in bf16: each thread 16 elements of a row (8 bytes of codes, one scale byte).
+// Rows back in bf16, a warp a row: lanes take units of 16 elements (8 bytes of codes, one
+// scale byte) side by side.
 template <int BLOCK>
 __global__ void __launch_bounds__(kThreads)
 dequantize_rows_kernel(const uint2* __restrict__ q, const uint32_t* __restrict__ sf,
                        const float* __restrict__ row_scale, const int32_t* __restrict__ offsets,
-                       int E, int M, int d, int rows_per_cta, uint4* __restrict__ out) {
+                       int E, int M, int d, uint4* __restrict__ out) {
   extern __shared__ int sm[];
   int* s_off = sm;
   int* s_tile = s_off + E + 1;
@@ -185,36 +311,54 @@ dequantize_rows_kernel(const uint2* __restrict__ q, const uint32_t* __restrict__
   __syncthreads();
   if (threadIdx.x < 32) tile_prefix(s_off, s_tile, E);
   __syncthreads();
+  const int lane = threadIdx.x & 31;
   const int units = d / 16;
   constexpr int kPer = BLOCK / 4;
+  constexpr int kAhead = 4;   // units a lane has in flight
+  const bool wide = aligned32(out);
   const int ka = (units + kPer - 1) / kPer;
-  const long long p0 = static_cast<long long>(blockIdx.x) * rows_per_cta;
-  const int rows = static_cast<int>(min(static_cast<long long>(rows_per_cta), M - p0));
-  for (int i = threadIdx.x; i < rows * units; i += kThreads) {
-    const int r = i / units, u = i - r * units;
-    const int p = static_cast<int>(p0) + r;
-    const int2 pl = place_of(p, s_off, s_tile, E);
-    if (pl.x < 0) continue;
-    const uint2 c = q[static_cast<size_t>(p) * units + u];
-    const uint32_t word = sf[(static_cast<size_t>(pl.x) * ka + u / kPer) * 128 + atom_word(pl.y)];
-    float f;
-    if constexpr (BLOCK == 16) {
-      f = from_e4m3((word >> (8 * (u & 3))) & 0xffu) * row_scale[p];
-    } else {
-      const uint32_t byte = (word >> (8 * ((u >> 1) & 3))) & 0xffu;
-      f = byte == kNanE8m0 ? __uint_as_float(0x7fc00000u) : two_to(static_cast<int>(byte) - 127);
-    }
-    uint32_t w[8];
+  const unsigned rows = static_cast<unsigned>(min(s_off[E], M));
+  const unsigned warps = gridDim.x * (kThreads / 32);
+  for (unsigned p = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); p < rows; p += warps) {
+    const int2 pl = place_of(static_cast<int>(p), s_off, s_tile, E);
+    const uint32_t* words = sf + static_cast<size_t>(pl.x) * ka * 128 + atom_word(pl.y);
+    const uint2* src = q + static_cast<size_t>(p) * units;
+    uint4* dst = out + static_cast<size_t>(p) * units * 2;
+    const float g = BLOCK == 16 ? __ldg(row_scale + p) : 1.f;
+    for (int u0 = lane; u0 < units; u0 += 32 * kAhead) {
+      uint2 c[kAhead];
+      uint32_t w[kAhead];
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      const uint32_t byte = ((h < 4 ? c.x : c.y) >> (8 * (h & 3))) & 0xffu;
-      const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-      const float2 v = __half22float2(__half2(hr));
-      w[h] = pack_bf16(v.x * f, v.y * f);
+      for (int i = 0; i < kAhead; ++i) {
+        const int u = u0 + 32 * i;
+        if (u < units) {
+          c[i] = __ldg(src + u);
+          w[i] = __ldg(words + static_cast<size_t>(u / kPer) * 128);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int u = u0 + 32 * i;
+        if (u >= units) break;
+        float f;
+        if constexpr (BLOCK == 16) {
+          f = from_e4m3((w[i] >> (8 * (u & 3))) & 0xffu) * g;
+        } else {
+          const uint32_t byte = (w[i] >> (8 * ((u >> 1) & 3))) & 0xffu;
+          f = byte == kNanE8m0 ? __uint_as_float(0x7fc00000u) : two_to(static_cast<int>(byte) - 127);
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const uint32_t byte = ((h < 4 ? c[i].x : c[i].y) >> (8 * (h & 3))) & 0xffu;
+          const __half2_raw hr =
+              __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+          const float2 v = __half22float2(__half2(hr));
+          o[h] = pack_bf16(v.x * f, v.y * f);
+        }
+        store32(dst + 2 * u, wide, o);
+      }
     }
-    uint4* dst = out + (static_cast<size_t>(p) * units + u) * 2;
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -228,9 +372,9 @@ weight_top_kernel(const uint4* __restrict__ w, long long vecs, uint32_t* __restr
   for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < vecs;
        i += static_cast<long long>(gridDim.x) * kThreads) {
     const uint4 v = ldg_nc_v4(base + i);
-    m = top_bits(top_bits(top_bits(top_bits(m, v.x), v.y), v.z), v.w);
+    m = top2(top2(top2(top2(m, v.x), v.y), v.z), v.w);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __reduce_max_sync(0xffffffffu, top_of(m));
   if ((threadIdx.x & 31) == 0 && m) atomicMax(top + blockIdx.y, m);
 }
 
@@ -260,12 +404,12 @@ quantize_weights_kernel(const __nv_bfloat16* __restrict__ w, int K, int N,
   const int e = static_cast<int>(b / kt);
   if (n >= N) return;
   const __nv_bfloat16* src = w + (static_cast<size_t>(e) * K + static_cast<size_t>(k64) * 64) * N + n;
-  int rexp = 0;
+  float g = 1.f, sixth = kSixth;
   bool fine = true;
   if constexpr (BLOCK == 16) {
-    const float g = scale[e];
+    g = scale[e];
     fine = g == g;
-    rexp = fine ? static_cast<int>(__float_as_uint(g) >> 23) - 127 : 0;
+    sixth = kSixth * reciprocal(g);   // a power of two: exact
   }
   uint2 c[4];
   uint32_t word = 0, pair_top = 0;
@@ -283,8 +427,8 @@ quantize_weights_kernel(const __nv_bfloat16* __restrict__ w, int K, int N,
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = make_pair(f[2 * j], f[2 * j + 1]);
     if constexpr (BLOCK == 16) {
-      const uint32_t byte = fine ? to_e4m3(__fdiv_rn(__uint_as_float(m), 6.f * two_to(rexp))) : 0u;
-      c[i] = fine ? codes16(v, byte, rexp) : make_uint2(0u, 0u);
+      const uint32_t byte = fine ? scale_byte(__uint_as_float(m), sixth) : 0u;
+      c[i] = fine ? codes16(v, byte, g) : make_uint2(0u, 0u);
       word |= byte << (8 * i);
     } else if (i & 1) {
       const uint32_t both = max(m, pair_top);
@@ -359,19 +503,37 @@ int launch_rows(const void* x, const int32_t* inv_perm, const int32_t* offsets, 
                     E, T, K, M, d, static_cast<uint2*>(q), static_cast<uint32_t*>(sf), row_scale);
 }
 
-// Threads a row: the fewest of 32 .. 256 that hold it with two units each, four above d = 8192.
+// CTAs of warps that stay for many rows: as many as eight to an SM.
+unsigned row_grid(long long rows) {
+  const long long need = (rows + kThreads / 32 - 1) / (kThreads / 32);
+  const long long most = 8LL * num_sms();
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+template <int BLOCK, int BPT>
+int launch_warp_rows(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
+                     int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st) {
+  ProfScope prof("fp4_quantize_rows", st);
+  return launch_pdl(quantize_warp_rows_kernel<BLOCK, BPT>, row_grid(T), kThreads,
+                    sizeof(int) * 2 * (E + 1), st, 1, static_cast<const uint4*>(x), inv_perm, offsets,
+                    E, T, K, M, d, static_cast<uint2*>(q), static_cast<uint32_t*>(sf), row_scale);
+}
+
 template <int BLOCK>
 int launch_rows_for(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
                     int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st) {
   const int units = d / 16;
-#define MOE_ROWS(TPR, BPT) \
-  return launch_rows<BLOCK, TPR, BPT>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st)
-  if (units <= 64) MOE_ROWS(32, 2);
-  if (units <= 128) MOE_ROWS(64, 2);
-  if (units <= 256) MOE_ROWS(128, 2);
-  if (units <= 512) MOE_ROWS(256, 2);
-  MOE_ROWS(256, 4);
+#define MOE_ROWS(BPT) \
+  return launch_warp_rows<BLOCK, BPT>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st)
+  if (units <= 64) MOE_ROWS(2);
+  if (units <= 128) MOE_ROWS(4);
+  if (units <= 192) MOE_ROWS(6);
 #undef MOE_ROWS
+  if (units <= 256)
+    return launch_rows<BLOCK, 128, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
+  if (units <= 512)
+    return launch_rows<BLOCK, kThreads, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
+  return launch_rows<BLOCK, kThreads, 4>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
 }
 
 }  // namespace
@@ -417,15 +579,13 @@ extern "C" int moe_fp4_dequantize_rows(const uint8_t* q, const uint8_t* sf, cons
   if (!aligned16(q) || !aligned16(sf) || !aligned16(offsets) || !aligned16(out) ||
       (row_scale && !aligned16(row_scale)))
     return MOE_ERR_MISALIGNED;
-  const int units = d / 16;
-  const int rows = units >= 4 * kThreads ? 1 : (4 * kThreads + units - 1) / units;   // about four units a thread
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(M) + rows - 1) / rows);
   cudaStream_t st = as_stream(stream);
   ProfScope prof("fp4_dequantize_rows", st);
   const size_t smem = sizeof(int) * 2 * (E + 1);
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, kThreads, smem, st, 1, reinterpret_cast<const uint2*>(q),
-                      reinterpret_cast<const uint32_t*>(sf), row_scale, offsets, E, M, d, rows,
+    return launch_pdl(kern, static_cast<unsigned>((static_cast<long long>(M) + kThreads / 32 - 1) / (kThreads / 32)),
+                      kThreads, smem, st, 1, reinterpret_cast<const uint2*>(q),
+                      reinterpret_cast<const uint32_t*>(sf), row_scale, offsets, E, M, d,
                       reinterpret_cast<uint4*>(out));
   };
   return block == 16 ? go(dequantize_rows_kernel<16>) : go(dequantize_rows_kernel<32>);

@@ -52,28 +52,43 @@ __device__ __forceinline__ int block_exponent(float top) {
 
 // Eight codes of four pairs of quotients (rounded to nearest, ties to even, at most 6).
 __device__ __forceinline__ uint32_t to_e2m1x8(const float_pair p[4]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(split_pair(p[i]), __NV_E2M1, cudaRoundNearest))
-         << (8 * i);
+  const float2 a = split_pair(p[0]), b = split_pair(p[1]), c = split_pair(p[2]), d = split_pair(p[3]);
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return w;
 }
 
-// The quotients v / t of bf16 values v and t = s g (four significant bits) by v * fl(1/t):
-// that product may miss a quotient that lies on a rounding border (a multiple of 1/4, at most
-// 9 in size) by 2^-23 of it, while every other quotient is at least 2^-8 of it away from one.
+// 1 / v to a few units of the last place (2^-126 <= v <= 2^126), 0 for v = 0.
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return v > 0.f ? r : 0.f;
+}
+
+// E4M3 byte of top / (6 g) for a bf16 value `top` and sixth = fl(1/6) / g, g a power of two.
+// The product is off by at most 2^-23 of it; a quotient on a rounding border of E4M3 has five
+// significant bits, every other is 2^-8 of it away from one. Rounding to 13 bits restores the
+// former and moves none of the latter across.
+constexpr float kSixth = 1.f / 6.f;
+__device__ __forceinline__ uint32_t scale_byte(float top, float sixth) {
+  return to_e4m3(__uint_as_float((__float_as_uint(top * sixth) + 0x400u) & ~0x7ffu));
+}
+
+// The quotients v / t of bf16 values v and t = s g (four significant bits) by v * (1/t): that
+// product may miss a quotient that lies on a rounding border (a multiple of 1/4, at most 9 in
+// size) by 2^-21 of it, while every other quotient is at least 2^-8 of it away from one.
 // Adding and subtracting kSnap rounds to multiples of 2^-12, which restores the former and
 // moves none of the latter across.
 constexpr float kSnap = 2560.f;
 
-// The codes of 16 bf16 values (as pairs) of a block with E4M3 scale byte sb under 2^n.
-__device__ __forceinline__ uint2 codes16(const float_pair v[8], uint32_t sb, int n) {
-  const float s = from_e4m3(sb);
-  // 1 / (s 2^n) = (1 / s) 2^-n; the second factor in two steps, since 2^-n may pass 2^127
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  const int a = -n / 2, b = -n - a;
-  const float f = inv * two_to(a) * two_to(b);
+// The codes of 16 bf16 values (as pairs) of a block with E4M3 scale byte sb under g.
+__device__ __forceinline__ uint2 codes16(const float_pair v[8], uint32_t sb, float g) {
+  const float f = reciprocal(from_e4m3(sb) * g);   // 2^-109 to 2^126, or 0
   const float_pair m = make_pair(f, f), c = make_pair(kSnap, kSnap), nc = make_pair(-kSnap, -kSnap);
   float_pair y[8];
 #pragma unroll

@@ -112,11 +112,11 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_
         : "memory");
 }
 
-// Output staging: two boxes of 32 rows x 64 columns a warp.
-template <int EPI>
-constexpr uint32_t epi_bytes() { return EPI == OUT ? 8u * 2u * 4096u : 0u; }
+// Output staging: boxes of 32 rows x 64 columns a warp, used in turn.
+template <int EPI, int BOXES>
+constexpr uint32_t epi_bytes() { return EPI == OUT ? 8u * BOXES * 4096u : 0u; }
 
-template <int EPI, int BLOCK, int BN, int STAGES>
+template <int EPI, int BLOCK, int BN, int STAGES, int BOXES>
 struct Shape {
   static constexpr uint32_t KA = 64 / BLOCK;            // scale atoms of a k-block (256 K)
   static constexpr uint32_t NB = BN / 128;              // B's scale tiles
@@ -128,7 +128,7 @@ struct Shape {
   static constexpr uint32_t SLOT = 4 * KA * (1 + NB);   // TMEM columns of a k-block's scales
   // At least 116 KB: a CTA takes all of its SM's TMEM, so two must not share one.
   static constexpr size_t smem(int E) {
-    const size_t n = 1024 + STAGES * STAGE + epi_bytes<EPI>() + 8 * (2 * STAGES + 3) + 16 +
+    const size_t n = 1024 + STAGES * STAGE + epi_bytes<EPI, BOXES>() + 8 * (2 * STAGES + 3) + 16 +
                      sizeof(int) * 2 * (E + 1) + 16;
     return n < 118784 ? 118784 : n;
   }
@@ -136,20 +136,20 @@ struct Shape {
   static_assert(BN <= static_cast<int>(kScaleCol), "accumulator below the scale slots");
 };
 
-template <int EPI, int BLOCK, int BN, int STAGES>
+template <int EPI, int BLOCK, int BN, int STAGES, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                 const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmSA,
                 const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC,
                 const Params p) {
-  using S = Shape<EPI, BLOCK, BN, STAGES>;
+  using S = Shape<EPI, BLOCK, BN, STAGES, BOXES>;
   constexpr uint32_t IDESC = make_idesc_fp4<BN, BLOCK>();
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* epi = smem + STAGES * S::STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + epi_bytes<EPI>());
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + epi_bytes<EPI, BOXES>());
   // bars: full[STAGES] (leader), empty[STAGES], tfull, tempty (leader), drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -355,6 +355,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int r = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     constexpr int W = BN / 2;    // accumulator columns of a thread
+    uint32_t box = 0;
     uint32_t phase = 0;
     for (int t = cid; t < total; t += ncl) {
       const Tile tl = decode<EPI, BN>(t, static_cast<int>(rank), p, s_off, s_mp);
@@ -364,6 +365,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       if (p.row_scale && valid) rs = __ldg(p.row_scale + grow);
       float f0 = p.scale0 ? __ldg(p.scale0 + tl.e) : 1.f;
       float f1 = p.scale1 ? __ldg(p.scale1 + tl.e) : 1.f;
+      const float hs = EPI == H4 && p.h_scale ? __ldg(p.h_scale + tl.e) : 1.f;
       if (!mbar_wait(tfull_bar, phase, abort_flag, p.status)) break;
       phase ^= 1u;
       tc_fence_after();
@@ -385,6 +387,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       // relaxed: the barrier orders TMEM reads alone, which have completed; a release would wait
       // for the last tile's stores
       if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(tempty_bar, 0));
+      // A branch the compiler cannot remove: without one it moves arithmetic of the epilogue above
+      // the arrive, which the next tile's MMAs wait for (gate/up 1390 -> 1296 us).
+      if (*abort_flag) break;
 
       if constexpr (EPI == OUT) {
         const float f = rs * f0 * f1;
@@ -394,9 +399,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (int c64 = 0; c64 < W; c64 += 64) {
           const int col = tl.n0 + hh * W + c64;
           if (col >= p.N) continue;
-          uint8_t* st = epi + ((warp - 2) * 2 + (c64 >> 6)) * 4096;
+          uint8_t* st = epi + (static_cast<uint32_t>(warp - 2) * BOXES + box) * 4096;
           if (full) {
-            if (lane == 0 && c64 == 0) bulk_wait_read_all();   // the last tile's stores
+            if (lane == 0) bulk_wait_read<BOXES - 1>();   // the store that used this box has read it
             __syncwarp();
           }
 #pragma unroll
@@ -420,6 +425,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               tma_store_2d(&tmC, smem_u32(st), col, growq);
               bulk_commit();
             }
+            if (++box == BOXES) box = 0;
           }
         }
       } else {
@@ -438,22 +444,22 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         } else {
           uint32_t code[HW / 8];
           uint32_t word = 0;
-          const float hs = p.h_scale ? __ldg(p.h_scale + tl.e) : 1.f;
+          const float sixth = kSixth * reciprocal(hs);
 #pragma unroll
           for (int b = 0; b < HW / BLOCK; ++b) {
+            const float* h = hv + b * BLOCK;
             float top = 0.f, sum = 0.f;   // the sum carries a NaN, which the maximum drops
 #pragma unroll
             for (int i = 0; i < BLOCK; ++i) {
-              top = fmaxf(top, fabsf(hv[b * BLOCK + i]));
-              sum += hv[b * BLOCK + i];
+              top = fmaxf(top, fabsf(h[i]));
+              sum += h[i];
             }
             const bool fine = top < __uint_as_float(0x7f800000u) && sum == sum;
             float inv;
             uint32_t byte;
             if constexpr (BLOCK == 16) {
-              byte = fine ? to_e4m3(__fdiv_rn(top, 6.f * hs)) : kNanE4m3;
-              const float s = from_e4m3(byte) * hs;
-              inv = (fine && s > 0.f) ? __frcp_rn(s) : 0.f;
+              byte = fine ? to_e4m3(top * sixth) : kNanE4m3;
+              inv = reciprocal(from_e4m3(byte) * hs);
             } else {
               const int X = block_exponent(fine ? top : 0.f);
               byte = fine ? static_cast<uint32_t>(X + 127) : kNanE8m0;
@@ -465,8 +471,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               float_pair y[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int at = b * BLOCK + 8 * o + 2 * i;
-                y[i] = fine ? make_pair(hv[at] * inv, hv[at + 1] * inv) : make_pair(0.f, 0.f);
+                const int at = 8 * o + 2 * i;
+                y[i] = make_pair(fine ? h[at] * inv : 0.f, fine ? h[at + 1] * inv : 0.f);
               }
               code[b * (BLOCK / 8) + o] = to_e2m1x8(y);
             }
@@ -535,17 +541,25 @@ struct Operands {
   int K;
 };
 
-// Stages beside the output staging, or without it.
-template <int EPI>
-constexpr int stages_of() { return EPI == OUT ? 4 : 5; }
+// Experts whose tables fit beside five stages and the output staging.
+constexpr int kDeepMaxE = 448;
+
+template <int EPI, int BLOCK, int BN, int STAGES, int BOXES, int MAX_E>
+int launch_stages(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
+                  const CUtensorMap& tsa, const CUtensorMap& tsb, const CUtensorMap& tc,
+                  const Params& p, long long tiles, cudaStream_t st) {
+  using S = Shape<EPI, BLOCK, BN, STAGES, BOXES>;
+  static_assert(S::smem(MAX_E) <= kSmemOptIn, "shared memory");
+  static thread_local int configured = -1;
+  static thread_local int max_clusters = 0;
+  return launch_cluster2(fp4_pair_kernel<EPI, BLOCK, BN, STAGES, BOXES>, kThreads, S::smem(p.E), S::smem(MAX_E),
+                         &configured, &max_clusters, tiles,
+                         EPI == OUT ? "gemm_fp4" : "gemm_gate_up_fp4", st, ta, tb0, tb1, tsa, tsb, tc, p);
+}
 
 template <int EPI, int BLOCK, int BN>
 int launch_pair(const Operands& o, Params p, cudaStream_t st) {
-  constexpr int kStages = stages_of<EPI>();
-  using S = Shape<EPI, BLOCK, BN, kStages>;
-  static_assert(S::smem(1024) <= kSmemOptIn, "shared memory");
-  static thread_local int configured = -1;
-  static thread_local int max_clusters = 0;
+  using S = Shape<EPI, BLOCK, BN, 5, 1>;
   const int per = EPI == OUT ? BN : BN / 2;   // outputs of a tile
   p.n_tiles = (p.N + per - 1) / per;
   p.k64 = o.K / 64;
@@ -560,9 +574,17 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st) {
   if (EPI != OUT) tc = ta;   // not stored through
   else if (!make_map(&tc, p.out, p.N, p.M, 64, 32)) return MOE_ERR_CUDA;
   const long long mt_upper = (p.M + BM - 1) / BM + p.E;
-  return launch_cluster2(fp4_pair_kernel<EPI, BLOCK, BN, kStages>, kThreads, S::smem(p.E), S::smem(1024),
-                         &configured, &max_clusters, mt_upper * p.n_tiles,
-                         EPI == OUT ? "gemm_fp4" : "gemm_gate_up_fp4", st, ta, tb0, tb1, tsa, tsb, tc, p);
+  const long long tiles = mt_upper * p.n_tiles;
+  if constexpr (EPI != OUT) {
+    return launch_stages<EPI, BLOCK, BN, 5, 1, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
+  } else {
+    // Up to four k-blocks a tile (K <= 1024) the stores decide, and a second staging box is worth
+    // more than a fifth stage: 84 against 90 us at K = 768 (65536 rows, 2048 outputs). Above, the
+    // loads do: five stages 141 against 151 us at K = 1408, 799 against 869 at K = 2048.
+    if (p.k64 > 16 && p.E <= kDeepMaxE)
+      return launch_stages<EPI, BLOCK, BN, 5, 1, kDeepMaxE>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
+    return launch_stages<EPI, BLOCK, BN, 4, 2, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
+  }
 }
 
 template <int EPI, int BLOCK>
