@@ -20,7 +20,8 @@ scratch, a block holds, between its passes, its input (the caller's, or the bloc
 before's out), out, the combined rows and the layer's codes; what it needs while it
 is at work it shares with the model's other blocks.
 
-Decoding (``MoEDecodeBlock``, experts on 4-bit weights):
+Decoding (``MoEDecodeBlock``, experts on 4-bit weights) and prefill (``MoEFp4Block``, experts
+on microscaled 4-bit floats, activations included):
     xn = block.norm(x);  logits = router(xn);  out = block.forward(logits)
 
 This module only allocates tensors and orders the calls; each step is a kernel
@@ -188,6 +189,106 @@ class MoEDecodeBlock:
         if self.shared:
             B.moe_grouped_ffn_w4(self.xn, self.s_offsets, self.w4["sgu"], self.w4["sd"],
                                  ws=self.ws_ffn, out=(self.ys, self.hs))
+            shared_y = self.ys
+        B.moe_norm_out(self.y, self.x, self.gain_out, self.topk_w, self.inv_perm, shared_y,
+                       self.gate, self.span, self.scale, self.eps, out=(self.out, None, None))
+        return self.out
+
+
+def fp4_weights(weights: Dict[str, torch.Tensor], block: int = 16):
+    """A layer's bf16 weights (as w4_weights takes them) as microscaled 4-bit floats in the form
+    moe_grouped_ffn_fp4 takes: {"wgu", "wd"[, "sgu", "sd"]}."""
+    def pack(gate, up, down):
+        (gq, gs, g), (uq, us, u), (dq, ds, d) = (B.moe_fp4_quantize_weights(w.contiguous(), block)
+                                                 for w in (gate, up, down))
+        return ((gq, uq, B.moe_fp4_pack_scales(gs, us, block), g, u),
+                (dq, B.moe_fp4_pack_scales(ds, block=block), d))
+
+    out = dict(zip(("wgu", "wd"), pack(weights["w_gate"], weights["w_up"], weights["w_down"])))
+    if "ws_gate" in weights:
+        shared = [weights[k].unsqueeze(0) for k in ("ws_gate", "ws_up", "ws_down")]
+        out.update(zip(("sgu", "sd"), pack(*shared)))
+    return out
+
+
+def fp4_h_scale(h: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    """h_scale [E] fp32 for moe_grouped_ffn_fp4 from a calibration pass's hidden rows h [M,I] (as
+    moe_grouped_ffn leaves them) and offsets: each expert's largest finite |H| / 2688, at least
+    2^-100; experts without a row (or whose rows are all zero) take the largest of all."""
+    E = offsets.numel() - 1
+    rows = torch.arange(h.shape[0], device=h.device)
+    e = torch.searchsorted(offsets[1:].long(), rows, right=True)
+    size = torch.nan_to_num(h.float(), 0.0, 0.0, 0.0).abs().amax(1)
+    top = torch.zeros(E + 1, device=h.device).scatter_reduce_(0, e, size, "amax")[:E]
+    return torch.where(top > 0, top, top.amax()).clamp(min=2688 * 2.0 ** -100) / 2688.0
+
+
+class MoEFp4Block:
+    """The block's forward for T tokens on experts in microscaled 4-bit floats (``w4`` from
+    ``fp4_weights``): the norm's rows are quantized while they are dispatched and both products
+    take 4-bit operands. ``h_scale`` [E] and ``sh_scale`` [1] (shared experts; ``fp4_h_scale``)
+    fix the hidden rows' scales, which saves a pass; without them, with block 16, each hidden row
+    takes its own. Saves nothing for a backward pass."""
+
+    def __init__(self, T: int, K: int, w4, gain_in: torch.Tensor,
+                 gain_out: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                 span: Optional[int] = None, scale: float = 1.0, eps: float = 1e-6,
+                 renorm: int = 1, block: int = 16, h_scale: Optional[torch.Tensor] = None,
+                 sh_scale: Optional[torch.Tensor] = None):
+        self.w4, self.K, self.renorm, self.block = w4, K, renorm, block
+        self.gain_in, self.gain_out, self.gate, self.span = gain_in, gain_out, gate, span
+        self.scale, self.eps = float(scale), float(eps)
+        self.h_scale, self.sh_scale = h_scale, sh_scale
+        dev = gain_in.device
+        d = gain_in.numel()
+        E, I, _ = w4["wgu"][0].shape
+        bf, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        e = lambda *s, dt: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
+        TK, n = T * K, E + 1
+        self.xn, self.rstd = e(T, d, dt=bf), e(T, dt=f32)
+        self.topk_idx, self.topk_w = e(T, K, dt=i32), e(T, K, dt=f32)
+        self.counts, self.offsets = e(E, dt=i32), e(E + 1, dt=i32)
+        self.perm, self.inv_perm = e(TK, dt=i32), e(TK, dt=i32)
+        self.splits, self.send, self.a2a, self.regroup = (e(n, dt=i32), e(TK, dt=i32),
+                                                          e(TK, dt=i32), e(TK, dt=i32))
+
+        def rows(M, E):
+            shapes = B._fp4_rows_shapes(M, d, E, block)
+            return (e(*shapes[0], dt=u8), e(*shapes[1], dt=u8),
+                    e(*shapes[2], dt=f32) if block == 16 else None)
+        self.rows = rows(TK, E)
+        self.y, self.out = e(TK, d, dt=bf), e(T, d, dt=bf)
+        self.ws_route = B.new_workspace(B.workspace_size(B.MOE_OP_ROUTE_PERMUTE_EP, T, E, K, 1), dev)
+        self.ws_ffn = B.new_workspace(
+            B.workspace_size(B.MOE_OP_GROUPED_FFN_FP4, TK, E, 1, 1, d, I), dev)
+        self.shared = "sgu" in w4
+        if self.shared:
+            Is = w4["sgu"][0].shape[1]
+            self.s_offsets = torch.tensor([0, T], dtype=i32, device=dev)
+            self.s_rows, self.ys = rows(T, 1), e(T, d, dt=bf)
+            self.ws_sffn = B.new_workspace(
+                B.workspace_size(B.MOE_OP_GROUPED_FFN_FP4, T, 1, 1, 1, d, Is), dev)
+        self.x = None
+
+    def norm(self, x: torch.Tensor) -> torch.Tensor:
+        self.x = x
+        B.moe_norm_in(x, self.gain_in, self.eps, out=(self.xn, self.rstd))
+        return self.xn
+
+    def forward(self, logits: torch.Tensor) -> torch.Tensor:
+        B.moe_route_permute_ep(logits, self.K, 1, self.renorm, host_splits=False, ws=self.ws_route,
+                               out=(self.topk_idx, self.topk_w, self.counts, self.offsets,
+                                    self.perm, self.inv_perm, self.splits, self.send, self.a2a,
+                                    self.regroup))
+        B.moe_fp4_quantize_rows(self.xn, self.offsets, self.block, self.inv_perm, self.K,
+                                out=self.rows)
+        B.moe_grouped_ffn_fp4(self.rows, self.offsets, self.w4["wgu"], self.w4["wd"], self.block,
+                              self.h_scale, ws=self.ws_ffn, out=self.y)
+        shared_y = None
+        if self.shared:
+            B.moe_fp4_quantize_rows(self.xn, self.s_offsets, self.block, out=self.s_rows)
+            B.moe_grouped_ffn_fp4(self.s_rows, self.s_offsets, self.w4["sgu"], self.w4["sd"],
+                                  self.block, self.sh_scale, ws=self.ws_sffn, out=self.ys)
             shared_y = self.ys
         B.moe_norm_out(self.y, self.x, self.gain_out, self.topk_w, self.inv_perm, shared_y,
                        self.gate, self.span, self.scale, self.eps, out=(self.out, None, None))

@@ -1715,7 +1715,9 @@ extern "C" int moe_grouped_gemm(const moe_bf16* x, const int32_t* offsets, int E
   if (!aligned16(x) || !aligned16(offsets) || !aligned16(w) || !aligned16(y)) return MOE_ERR_MISALIGNED;
   if (!ws || ws_bytes < kWorkspaceHeader || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   if (cc_major() < 10) return MOE_ERR_UNSUPPORTED;
-  const int bn = pair_bn(N);
+  // 256-wide tiles even where 128-wide ones leave fewer columns idle: 32766 rows of 2048 to 1400,
+  // 640 and 384 outputs take 167, 91 and 72 us against 220, 113 and 79.
+  const int bn = N > 128 && MOE_PAIR_BN_MAX >= 256 ? 256 : 128;
   CUtensorMap ta, tb, tc;
   if (!make_map(&ta, x, K, M, 64, BM) || !make_map(&tc, y, N, M, 64, 32) ||
       !(trans ? make_map3(&tb, w, K, N, E, 64, bn / 2) : make_map3(&tb, w, N, K, E, 64, 64)))
