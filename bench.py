@@ -65,7 +65,7 @@ def parse():
     ap.add_argument("--cpu-sample-tokens", type=int, default=0)
     ap.add_argument("--profile-case", choices=["gemm", "gemm_ragged", "gemm_l2", "gemm_drafter",
                                                "gemm_drafter64", "layer", "hbm", "routing",
-                                               "combine_side", "fp8", "block"],
+                                               "combine_side", "fp8", "fp4", "block"],
                     default=None,
                     help="run a small fixed case twice for an ncu capture and exit")
     return ap.parse_args()
@@ -91,6 +91,10 @@ def profile_case(which: str):
              ~0.4 GB on the device.
     fp8:     the MXFP8 forward (weight quantization, then moe_grouped_ffn_fp8) on E=64 experts
              x 512 rows (d=2048, I=768), run twice; ~1.5 GB on the device.
+    fp4:     rows quantized to microscaled 4-bit floats and read back, the experts on them
+             (moe_grouped_ffn_fp4, fixed hidden scales) and the grouped products by themselves
+             (moe_grouped_gemm_fp4, moe_grouped_gemm, moe_grouped_gemm_wgrad) on E=64 experts x
+             512 rows (d=2048, I=768), run twice; ~2 GB on the device.
     combine_side: the combine, its backward and the dispatch backward at the qwen3 workload's
              full size (T=8192, d=2048, K=8; the routing of the qwen3 inputs), on synthetic
              expert outputs and gradients (~1.1 GB on the device), run twice, with 256 MiB
@@ -192,6 +196,30 @@ def profile_case(which: str):
             wgu = B.moe_mxfp8_quantize_weights(wg, wu)
             wdq = B.moe_mxfp8_quantize_weights(wd)
             B.moe_grouped_ffn_fp8(xp, off, wgu, wdq)
+    elif which == "fp4":
+        from grouped_gemm_moe_gb300 import block as BL
+        E, d, I, rows = 64, 2048, 768, 512
+        M = E * rows
+        bf = torch.bfloat16
+        rnd = lambda *s, sc=1.0: (torch.randn(*s, device=dev, generator=g) * sc).to(bf)  # noqa: E731
+        off = (torch.arange(E + 1, dtype=torch.int32) * rows).to(dev)
+        xp, h = rnd(M, d), rnd(M, I, sc=0.5)
+        w = {"w_gate": rnd(E, d, I, sc=0.02), "w_up": rnd(E, d, I, sc=0.02),
+             "w_down": rnd(E, I, d, sc=0.02)}
+        w4 = BL.fp4_weights(w)
+        h_scale = torch.full((E,), 8.0 / 2688, device=dev)
+        flops = {"gemm_gate_up_fp4": 4 * M * d * I, "gemm_fp4": 2 * M * d * I,
+                 "gemm_down": 2 * M * d * I, "gemm_wgrad_down": 2 * M * d * I}
+        for it in range(2):
+            if it == 1:
+                torch.cuda.synchronize()
+                B.moe_profile_start(64)
+            x4 = B.moe_fp4_quantize_rows(xp, off)
+            B.moe_fp4_dequantize_rows(x4, off)
+            y = B.moe_grouped_ffn_fp4(x4, off, w4["wgu"], w4["wd"], h_scale=h_scale)
+            B.moe_grouped_gemm_fp4(B.moe_fp4_quantize_rows(h, off), off, w4["wd"])
+            B.moe_grouped_gemm(h, off, w["w_down"])
+            B.moe_grouped_gemm_wgrad(h, y, off)
     elif which == "combine_side":
         cfg = W.CONFIGS["qwen3"]
         inp = W.make_inputs(cfg, with_backward=False)

@@ -1060,7 +1060,7 @@ def moe_grouped_ffn_w4(x: torch.Tensor, offsets: torch.Tensor, wgu, wd,
 # ---------------------------------------------------------------- products grouped by expert
 def _call(name: str, dev: torch.device, *args):
     """The entry point on dev's current stream, with dev the current device."""
-    fn = getattr(load(), name)
+    fn = getattr(_lib or load(), name)
     if dev.index == torch._C._cuda_getDevice():
         return _check(name, fn(*args, _stream(dev)))
     with torch.cuda.device(dev):
@@ -1083,8 +1083,11 @@ def moe_grouped_gemm(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor, tr
     M, K = x.shape
     dev = x.device
     E = _experts_of(offsets, dev)
-    N = w.shape[1] if trans else w.shape[2]
-    _shaped(w, torch.bfloat16, (E, N, K) if trans else (E, K, N), "w", dev)
+    e, a, b = w.shape
+    N = a if trans else b
+    if (e, b if trans else a) != (E, K) or w.device != dev:
+        raise ValueError(f"w must have shape {(E, N, K) if trans else (E, K, N)} on {dev}, got "
+                         f"{tuple(w.shape)} on {w.device}")
     ws = _need_ws(ws, WORKSPACE_HEADER, dev)
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
@@ -1105,8 +1108,9 @@ def moe_grouped_gemm_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Ten
     dev = x.device
     E = _experts_of(offsets, dev)
     _need(dy, torch.bfloat16, 2, "dy")
-    N = dy.shape[1]
-    _shaped(dy, torch.bfloat16, (M, N), "dy", dev)
+    rows, N = dy.shape
+    if rows != M or dy.device != dev:
+        raise ValueError(f"dy must have shape {(M, N)} on {dev}, got {tuple(dy.shape)} on {dy.device}")
     ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_GEMM_WGRAD, M, E, 1, 1, K, N) if ws is None else 0,
                   dev)
     if out is None:

@@ -235,43 +235,42 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued[s] = 0;
+      unsigned long long issued = 0;   // k-blocks
       bool ok = true;
+      const uint32_t full0 = map_to_rank(full_bar(0), 0);   // the leader's
+      const CUtensorMap* mb = EPI != OUT && rank ? &tmB1 : &tmB0;
       for (int t = cid; t < total && ok; t += ncl) {
         const Tile tl = decode<EPI, BN>(t, static_cast<int>(rank), p, s_off, s_mp);
         // a follower without rows (the expert's end) loads no A: its rows are not stored
         const int rows1 = leader ? s_off[tl.e + 1] - (tl.row0 + BM) : tl.rows;
         const bool load_a = leader || rows1 > 0;
         const uint32_t bytes = 2 * (S::B + S::SB) + (rows1 > 0 ? 2u : 1u) * (S::A + S::SA);
+        const int brow = EPI == OUT ? tl.n0 + static_cast<int>(rank) * (BN / 2) : tl.n0;
+        const int a_tile = 2 * tl.mg + static_cast<int>(rank);
+        const int b_tile = tl.e * p.sf_tiles + tl.nt * static_cast<int>(S::NB);
         for (int kb = 0; kb < k_blocks; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
           if (leader) mbar_expect_tx(full_bar(stage), bytes);   // both CTAs' boxes
-          const uint32_t fb = map_to_rank(full_bar(stage), 0);
+          const uint32_t fb = full0 + 8u * stage;
           const uint32_t sa = smem_base + stage * S::STAGE;
-          const uint32_t sb = sa + S::A;
-          const uint32_t ssa = sb + S::B;
+          const uint32_t ssa = sa + S::A + S::B;
+          const int ka = kb * static_cast<int>(S::KA);
           if (load_a) {
             tma_load_2d_pair(sa, &tmA, fb, kb * 128, tl.row0);
-            tma_load_3d_pair(ssa, &tmSA, fb, 0, kb * static_cast<int>(S::KA),
-                             2 * tl.mg + static_cast<int>(rank));
+            tma_load_3d_pair(ssa, &tmSA, fb, 0, ka, a_tile);
           }
-          if constexpr (EPI == OUT)
-            tma_load_3d_pair(sb, &tmB0, fb, kb * 128, tl.n0 + static_cast<int>(rank) * (BN / 2), tl.e);
-          else
-            tma_load_3d_pair(sb, rank ? &tmB1 : &tmB0, fb, kb * 128, tl.n0, tl.e);
-          tma_load_3d_pair(ssa + S::SA, &tmSB, fb, 0, kb * static_cast<int>(S::KA),
-                           tl.e * p.sf_tiles + tl.nt * static_cast<int>(S::NB));
-          issued[stage] += 1;
+          tma_load_3d_pair(sa + S::A, mb, fb, kb * 128, brow, tl.e);
+          tma_load_3d_pair(ssa + S::SA, &tmSB, fb, 0, ka, b_tile);
+          ++issued;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (leader) {
         // the leader's full barriers count both CTAs' loads: wait for the last phases
         for (int s = 0; s < STAGES; ++s) {
-          if (!issued[s]) continue;
-          const uint32_t par = (issued[s] - 1u) & 1u;
+          const unsigned long long uses = (issued + STAGES - 1 - s) / STAGES;
+          if (!uses) continue;
+          const uint32_t par = static_cast<uint32_t>(uses - 1) & 1u;
           const uint64_t t0 = globaltimer();
           while (!mbar_try(full_bar(s), par) && globaltimer() - t0 < kTimeoutNs) {
           }
@@ -295,8 +294,6 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       int fresh = kRing;   // scale slots not yet used
       bool ok = true;
       for (int j = 0; j < my_tiles && ok; ++j) {
-        if (!mbar_wait(tempty_bar, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
         for (int kb = 0; kb < k_blocks; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) { ok = false; break; }
           // the slot's last readers, the MMAs of kRing blocks ago, have completed
@@ -312,11 +309,16 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
           for (uint32_t k = 0; k < S::KA; ++k) tc_cp_pair_32x128(slot + 4 * k, sf + 32 * k);
 #pragma unroll
-          for (uint32_t j = 0; j < S::NB; ++j)
+          for (uint32_t b = 0; b < S::NB; ++b)
 #pragma unroll
             for (uint32_t k = 0; k < S::KA; ++k)
-              tc_cp_pair_32x128(slot + 4 * S::KA + 4 * (k * S::NB + j),
-                                sf + S::SA / 16 + 32 * (j * S::KA + k));
+              tc_cp_pair_32x128(slot + 4 * S::KA + 4 * (k * S::NB + b),
+                                sf + S::SA / 16 + 32 * (b * S::KA + k));
+          // the accumulator, once the first block's operands and scales are in place
+          if (kb == 0) {
+            if (!mbar_wait(tempty_bar, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+          }
           const uint64_t da = desc_op + static_cast<uint32_t>(stage) * (S::STAGE / 16);
           const int steps = min(4, p.k64 - 4 * kb);
           auto step = [&](uint32_t kk, uint32_t acc) {   // 64 K: 32 bytes of a row
