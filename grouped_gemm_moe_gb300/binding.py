@@ -1144,7 +1144,9 @@ def _given(t, dtype, shape, name: str, dev):
     """_shaped for a tensor that has to be there."""
     if t is None:
         raise ValueError(f"{name} is missing")
-    _shaped(t, dtype, shape, name, dev)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev.index):
+        _shaped(t, dtype, shape, name, dev)
 
 
 def _fp4_rows(rows, E: int, block: int, dev):
@@ -1299,8 +1301,9 @@ def moe_grouped_ffn_fp4(rows, offsets: torch.Tensor, wgu, wd, block: int = 16,
     _given(gsf, torch.uint8, (E, I // 64, _fp4_atoms(d, block), 512), "gate and up scales", dev)
     _given(down, torch.uint8, (E, d, I // 2), "down codes", dev)
     _given(dsf, torch.uint8, (E, -(-d // 128), _fp4_atoms(I, block), 512), "down scales", dev)
-    gscale, uscale, dscale = (_fp4_factor(t, E, block, n, dev) for t, n in
-                              ((gscale, "gate scale"), (uscale, "up scale"), (dscale, "down scale")))
+    gscale = _fp4_factor(gscale, E, block, "gate scale", dev)
+    uscale = _fp4_factor(uscale, E, block, "up scale", dev)
+    dscale = _fp4_factor(dscale, E, block, "down scale", dev)
     if h_scale is not None:
         if block == 32:
             raise ValueError("h_scale goes with block 16")

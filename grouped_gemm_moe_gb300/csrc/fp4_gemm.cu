@@ -569,12 +569,16 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st) {
   const uint64_t atoms = k_atoms(o.K, BLOCK), kb = o.K / 2;
   CUtensorMap ta, tb0, tb1, tsa, tsb, tc;
   if (!make_map_u8(&ta, o.a, kb, p.M, 128, BM) || !make_map3_u8(&tb0, o.b0, kb, p.N, p.E, 128, BN / 2) ||
-      !make_map3_u8(&tb1, o.b1, kb, p.N, p.E, 128, BN / 2) ||
       !make_map_scales(&tsa, o.sfa, atoms, row_tiles(p.M, p.E), S::KA, 1) ||
       !make_map_scales(&tsb, o.sfb, atoms, static_cast<uint64_t>(p.E) * p.sf_tiles, S::KA, S::NB))
     return MOE_ERR_CUDA;
-  if (EPI != OUT) tc = ta;   // not stored through
-  else if (!make_map(&tc, p.out, p.N, p.M, 64, 32)) return MOE_ERR_CUDA;
+  if (EPI == OUT) {
+    tb1 = tb0;   // not read
+    if (!make_map(&tc, p.out, p.N, p.M, 64, 32)) return MOE_ERR_CUDA;
+  } else {
+    tc = ta;     // not stored through
+    if (!make_map3_u8(&tb1, o.b1, kb, p.N, p.E, 128, BN / 2)) return MOE_ERR_CUDA;
+  }
   const long long mt_upper = (p.M + BM - 1) / BM + p.E;
   const long long tiles = mt_upper * p.n_tiles;
   if constexpr (EPI != OUT) {
