@@ -72,6 +72,21 @@ def test_weight_gradient(K, N, counts):
     _dw_close(f64(dw), one + _wgrad(x2, dy2, offsets), counts)
 
 
+def test_many_experts():
+    """Past the expert counts up to which the deeper rings' tables fit."""
+    rng = np.random.default_rng(600)
+    counts = rng.integers(0, 4, size=600)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    M = int(offsets[-1])
+    x, dy = O.round_bf16(rng.normal(size=(M, 72))), O.round_bf16(rng.normal(size=(M, 40)))
+    w = O.round_bf16(rng.normal(size=(600, 72, 40)))
+    off = to_dev(offsets, I32)
+    assert_bf16_close(f64(B.moe_grouped_gemm(to_dev(x, BF), off, to_dev(w, BF))),
+                      F.grouped_product(x, offsets, w), "y")
+    _dw_close(f64(B.moe_grouped_gemm_wgrad(to_dev(x, BF), to_dev(dy, BF), off)), _wgrad(x, dy, offsets),
+              [4])
+
+
 def test_gradients_by_differences():
     """loss = sum(y r): central differences of the float64 product against the three calls."""
     rng = np.random.default_rng(2)
