@@ -586,7 +586,7 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st) {
     tc = ta;     // not stored through
     if (!make_map3_u8(&tb1, o.b1, kb, p.N, p.E, 128, BN / 2)) return MOE_ERR_CUDA;
   }
-  const long long mt_upper = (p.M + BM - 1) / BM + p.E;
+  const long long mt_upper = (static_cast<long long>(p.M) + BM - 1) / BM + p.E;
   const long long tiles = mt_upper * p.n_tiles;
   if constexpr (EPI != OUT) {
     return launch_stages<EPI, BLOCK, BN, 5, 1, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);

@@ -60,7 +60,8 @@ enum Kind : int {
   BWD_DH = 2,      // dH = dY Wd^T; epilogue dG, dU from saved GU
   BWD_DX = 3,      // dX = [dG|dU] [Wg|Wu]^T
   WGRAD_GU = 4,    // [dWg|dWu] = X^T [dG|dU]   (ragged K)
-  WGRAD_D = 5      // dWd = H^T dY              (ragged K)
+  WGRAD_D = 5,     // dWd = H^T dY              (ragged K)
+  WGRAD_X = 6      // dW = X^T dY by itself: both operands' straddling steps padded, may add to dW
 };
 
 constexpr int BM = 128;
@@ -106,10 +107,7 @@ struct Params {
   int* status;             // workspace status word
   PadJob pad[2];           // BWD_DH: the weight gradients' pads of X and H (a == null: none)
   int kb_half;             // BWD_DX: k-blocks of the dG half of K (then as many of the dU half)
-  int accumulate;          // weight gradients: add to dW (an expert without rows adds nothing)
-  int pad_b;               // dW by itself: B's straddling steps are zero-padded too (maps tmB2: B in
-                           // 16-row boxes, tmC1: the pads), so an Inf or NaN in the next expert's
-                           // rows meets no zero of A
+  int accumulate;          // WGRAD_X: add to dW (an expert without rows adds nothing)
   int tag_mode;            // kTagNone, kTagWrite (data part's dH) or kTagCheck (weight part)
   uint32_t tag[kTagWords]; // the backward's scratch tag: magic, M, E, d, I, offsets (low 32 bits)
   uint8_t* hq;             // MXFP8 gate/up: E4M3 of H for the down projection (null: not fused)
@@ -973,7 +971,7 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
                                const __grid_constant__ CUtensorMap tmC1,
                                const __grid_constant__ CUtensorMap tmA16,
                                const __grid_constant__ CUtensorMap tmP, const Params p) {
-  static_assert(KIND == WGRAD_GU || KIND == WGRAD_D, "pair weight-gradient kernel");
+  static_assert(KIND == WGRAD_GU || KIND == WGRAD_D || KIND == WGRAD_X, "pair weight-gradient kernel");
   constexpr int BN = 256;
   constexpr uint32_t MN_ATOM = 64 * 128;
   constexpr uint32_t A_BYTES = BM * BK * 2;
@@ -1081,14 +1079,16 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
             // K16 steps past it are neither loaded nor read
             const int nfull = kvalid >> 4;
             const uint32_t steps = static_cast<uint32_t>(nfull + 1) * 2 * 2048u;   // one operand's boxes
-            if (leader) mbar_expect_tx(fb, 2 * (steps + (p.pad_b ? steps : B_BYTES)));
+            // WGRAD_X: B's straddling step is zero-padded too (tmB2: B in 16-row boxes, tmC1: the
+            // pads), so that an Inf or NaN in the next expert's rows meets no zero of A
+            if (leader) mbar_expect_tx(fb, 2 * (steps + (KIND == WGRAD_X ? steps : B_BYTES)));
 #pragma unroll
             for (int atom = 0; atom < 2; ++atom) {
               const uint32_t da = sa + atom * MN_ATOM;
               const int x = tl.m0 + 64 * atom;
               for (int kk = 0; kk < nfull; ++kk) tma_load_2d_pair(da + kk * 2048, &tmA16, fr, x, ky + 16 * kk);
               tma_load_2d_pair(da + nfull * 2048, &tmP, fr, x, tl.e * 16);
-              if (KIND == WGRAD_D && p.pad_b) {
+              if constexpr (KIND == WGRAD_X) {
                 const uint32_t db = sa + A_BYTES + atom * MN_ATOM;
                 const int xb = nb + 64 * atom;
                 for (int kk = 0; kk < nfull; ++kk) tma_load_2d_pair(db + kk * 2048, &tmB2, fr, xb, ky + 16 * kk);
@@ -1096,7 +1096,7 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
               }
             }
           }
-          if (!(KIND == WGRAD_D && p.pad_b && (kvalid & 15) != 0)) {
+          if (KIND != WGRAD_X || (kvalid & 15) == 0) {
             const CUtensorMap* mb = tl.part ? &tmB2 : &tmB;   // dG or dU half (gate/up)
             tma_load_2d_pair(sa + A_BYTES, mb, fr, nb, ky);
             tma_load_2d_pair(sa + A_BYTES + MN_ATOM, mb, fr, nb + 64, ky);
@@ -1193,7 +1193,7 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
     for (int t = cid; t < total; t += ncl) {
       const WTile tl = decode_wgrad_pair<KIND>(t, static_cast<int>(rank), p, s_off);
       const bool empty = (tl.nkb == 0);   // expert without rows: its gradient is zero
-      if (empty && p.accumulate) continue;
+      if (KIND == WGRAD_X && empty && p.accumulate) continue;
       if (!empty) {
         if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status)) break;
         tc_fence_after();
@@ -1225,9 +1225,8 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
         __syncwarp();
         if (lane == 0) {
           // 3-D maps [E][rows][cols] of dW: rows and columns past the expert's are clipped
-          const CUtensorMap* tmC = tl.part ? &tmC1 : &tmC0;
-          if (p.accumulate) tma_add_3d(tmC, smem_u32(stg), tl.n0 + c, mrow, tl.e);
-          else tma_store_3d(tmC, smem_u32(stg), tl.n0 + c, mrow, tl.e);
+          if (KIND == WGRAD_X && p.accumulate) tma_add_3d(&tmC0, smem_u32(stg), tl.n0 + c, mrow, tl.e);
+          else tma_store_3d(tl.part ? &tmC1 : &tmC0, smem_u32(stg), tl.n0 + c, mrow, tl.e);
           bulk_commit();
         }
         // Spread the tile's stores over ~40% of the next tile's MMA time (~0.3 us of
@@ -1344,7 +1343,9 @@ int launch_pair_wgrad_stages(const CUtensorMap& a, const CUtensorMap& b, const C
                          pair_wgrad_smem_bytes<STAGES>(p.E),
                          pair_wgrad_smem_bytes<STAGES>(STAGES == 6 ? kWgradPair6MaxE : 1024),
                          &configured, &max_clusters, tiles,
-                         KIND == WGRAD_GU ? "gemm_wgrad_gate_up" : "gemm_wgrad_down", st, a, b,
+                         KIND == WGRAD_GU ? "gemm_wgrad_gate_up" : KIND == WGRAD_D ? "gemm_wgrad_down"
+                                                                                  : "gemm_wgrad",
+                         st, a, b,
                          b2, c0, c1, a16, pad, p);
 }
 
@@ -1783,9 +1784,8 @@ extern "C" int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, con
   p.n_tiles = (N + 255) / 256;
   p.outf0 = dw;
   p.accumulate = accumulate != 0;
-  p.pad_b = 1;
   p.status = static_cast<int*>(ws);
-  return launch_pair_wgrad<WGRAD_D>(ta, tb, tb16, tc, tpb, ta16, tpa, p,
+  return launch_pair_wgrad<WGRAD_X>(ta, tb, tb16, tc, tpb, ta16, tpa, p,
                                     static_cast<long long>(E) * p.m_tiles * p.n_tiles, st);
 }
 
