@@ -704,7 +704,7 @@ int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, const int32_t*
  *   x [T,d] bf16, inv_perm [T*K] int32, offsets [E+1] int32 in.
  *   q [T*K, d/2] uint8, sf [tiles, KA, 512] uint8 (tiles for M = T*K), row_scale [T*K] fp32
  *   (block 16; NULL with block 32) out. Scales of rows past an expert's last row are not
- *   written. 64 <= d <= 16384, K <= 32, E <= 1024. */
+ *   written (rows past offsets[E] get codes and a factor alone, which no product reads). 64 <= d <= 16384, K <= 32, E <= 1024. */
 int moe_fp4_quantize_rows(const moe_bf16* x, const int32_t* inv_perm, int T, int K,
                           const int32_t* offsets, int E, int d, int block, uint8_t* q, uint8_t* sf,
                           float* row_scale, void* stream);
