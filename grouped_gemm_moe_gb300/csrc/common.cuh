@@ -234,6 +234,13 @@ __device__ __forceinline__ void report_status(int* status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
 
+// The experts' backward in two parts leaves a record in the workspace header (int32 words from
+// kTagFirst on, a magic word first) that vouches for what its data part left in the workspace past
+// the header. Every operation that writes there ends the record, by one thread of a launch of its
+// own after pdl_wait().
+constexpr int kTagFirst = 4;
+__device__ __forceinline__ void end_backward_record(void* ws) { static_cast<int32_t*>(ws)[kTagFirst] = 0; }
+
 // Debug builds (-DMOE_DEBUG_CHECKS): every gathered or scattered index is
 // range-checked before its access and the GEMM tile scheduler checks the
 // expert offsets. A failed check skips or redirects the access to a valid row

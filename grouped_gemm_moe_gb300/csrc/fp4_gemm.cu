@@ -193,6 +193,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   }
   pdl_wait();   // offsets and operands come from earlier launches
   pdl_launch_dependents();
+  // H goes to the workspace
+  if (EPI != OUT && blockIdx.x == 0 && threadIdx.x == 0) end_backward_record(p.status);
   for (int e = threadIdx.x; e <= p.E; e += kThreads) s_off[e] = __ldg(p.offsets + e);
   __syncthreads();
   bool offs_ok = true;

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kFrontThreads, 1) route_hist_kernel(const Fron
   float* swt = reinterpret_cast<float*>(sid + a.ct * K);   // [ct*K] weights
 
   pdl_enter();   // logits come from an earlier launch; the next launch may be scheduled now
+  if (blockIdx.x == 0 && threadIdx.x == 0) end_backward_record(a.status);
   const Chunk ch = chunk_of(a, blockIdx.x);
   const int n = (ch.t1 - ch.t0) * K;
   const int w = threadIdx.x >> 5;

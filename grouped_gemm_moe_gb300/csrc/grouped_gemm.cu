@@ -82,10 +82,11 @@ struct PadJob {
 // the workspace header (words kTagFirst.. after the status word); the weight
 // part's kernels compare that record with their own arguments and, on a
 // mismatch (no data part on this workspace, other sizes or other offsets),
-// report MOE_ERR_DEVICE_CHECK and compute nothing.
+// report MOE_ERR_DEVICE_CHECK and compute nothing. Other operations that write into a
+// workspace end the record (end_backward_record); the MXFP8 experts' gate/up launch does
+// so by writing one of zeros.
 constexpr int kTagNone = 0, kTagWrite = 1, kTagCheck = 2;
 constexpr int kTagWords = 6;
-constexpr int kTagFirst = 4;                  // int32 index in the workspace header
 constexpr uint32_t kTagMagic = 0x4D6F4542u;
 
 struct Params {
@@ -108,7 +109,7 @@ struct Params {
   PadJob pad[2];           // BWD_DH: the weight gradients' pads of X and H (a == null: none)
   int kb_half;             // BWD_DX: k-blocks of the dG half of K (then as many of the dU half)
   int accumulate;          // WGRAD_X: add to dW (an expert without rows adds nothing)
-  int tag_mode;            // kTagNone, kTagWrite (data part's dH) or kTagCheck (weight part)
+  int tag_mode;            // kTagNone, kTagWrite (data part's dH, MXFP8 gate/up) or kTagCheck (weight part)
   uint32_t tag[kTagWords]; // the backward's scratch tag: magic, M, E, d, I, offsets (low 32 bits)
   uint8_t* hq;             // MXFP8 gate/up: E4M3 of H for the down projection (null: not fused)
   uint8_t* hsf;            //   and H's scale atoms (row tiles in the tile list's m-tile order)
@@ -1264,9 +1265,10 @@ grouped_gemm_pair_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
 // The zero-padded straddling steps of both operands (a CTA per expert and operand), for weight
 // gradients that no dH launch precedes.
 __global__ void __launch_bounds__(128)
-pad_steps_kernel(const int32_t* offsets, int M, const PadJob a, const PadJob b) {
+pad_steps_kernel(const int32_t* offsets, int M, const PadJob a, const PadJob b, void* ws) {
   __shared__ int s_off[2];
   pdl_enter();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) end_backward_record(ws);
   if (threadIdx.x < 2) s_off[threadIdx.x] = __ldg(offsets + blockIdx.x + threadIdx.x);
   __syncthreads();
   if (!index_ok(s_off[0] >= 0 && s_off[0] <= s_off[1] && s_off[1] <= M)) return;
@@ -1764,7 +1766,7 @@ extern "C" int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, con
     ProfScope prof("gemm_pad_steps", st);
     const int rc = launch_pdl(pad_steps_kernel, dim3(E, 2), 128, 0, st, 1, offsets, M,
                               PadJob{reinterpret_cast<const __nv_bfloat16*>(x), pad_x, K},
-                              PadJob{reinterpret_cast<const __nv_bfloat16*>(dy), pad_y, N});
+                              PadJob{reinterpret_cast<const __nv_bfloat16*>(dy), pad_y, N}, ws);
     if (rc) return rc;
   }
   CUtensorMap ta, tb, tc, ta16, tb16, tpa, tpb;
@@ -1855,11 +1857,13 @@ extern "C" int moe_grouped_ffn_fp8(const moe_bf16* xp, const int32_t* offsets, i
   p.ld_out = I;
   p.hq = hq;
   p.hsf = hsf;
+  p.tag_mode = kTagWrite;   // of zeros: the scratch holds no data part any more
   rc = launch_pair_depth<FWD_GATEUP, 256, true>(ta, tb0, tb1, tc0, tc1, tc2, ts, p,
                                                  mt_upper * p.n_tiles, st);
   if (rc) return rc;
   p.hq = nullptr;
   p.hsf = nullptr;
+  p.tag_mode = kTagNone;
   // down on 256 x 256 pair tiles (256 x 128 when d is an odd multiple of 128)
   const int bn = pair_bn(d);
   if (!make_map_u8(&ta, hq, I, M, 128, BM) ||

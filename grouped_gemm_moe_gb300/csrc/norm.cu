@@ -519,6 +519,7 @@ struct BackwardArgs {
   float* part_gate0;
   float* part_gate1;
   float* row_dot;         // per-row gate gradients (gate of one column)
+  void* ws;               // the workspace of part_* and row_dot
   int T, span, chunk;
   float scale, inv_d;
   int nv, G;
@@ -541,6 +542,7 @@ constexpr int ring_threads(int V) { return V == 1 ? 1024 : 512; }
 template <int V, bool RES, bool NORM, int GATE>
 __global__ void __launch_bounds__(ring_threads(V), 1) norm_backward_kernel(BackwardArgs A) {
   pdl_enter();
+  if (blockIdx.x == 0 && threadIdx.x == 0) end_backward_record(A.ws);
   constexpr int kStages = ring_stages(V), kArrays = RES ? 3 : 2;
   constexpr bool kVec = GATE == kGateVector;
   extern __shared__ uint4 ring[];   // [stage][array][v][thread]
@@ -838,6 +840,7 @@ int launch_backward(const char* name, BackwardArgs a, int T, int d, bool norm, i
   const BackwardPlan p = plan_backward(T, d, a.dres ? 3 : 2);
   float* scratch = reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspaceHeader);
   const size_t slots = static_cast<size_t>(p.chunks.workers) * d;
+  a.ws = ws;
   a.part_gain = scratch;
   a.part_gate0 = scratch + slots;
   a.part_gate1 = scratch + 2 * slots;

@@ -76,8 +76,10 @@ __device__ __forceinline__ void warp_count(const int (&ev)[kSteps], int* wh) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-hist_kernel(const int32_t* __restrict__ idx, int E, ChunkGeom g, int32_t* __restrict__ hist) {
+hist_kernel(const int32_t* __restrict__ idx, int E, ChunkGeom g, int32_t* __restrict__ hist,
+            void* ws) {   // ws: the workspace that hist lies in, or null
   pdl_enter();
+  if (ws && blockIdx.x == 0 && threadIdx.x == 0) end_backward_record(ws);
   extern __shared__ int smem[];
   int* wh = smem;  // [kWarps][E]
   for (int i = threadIdx.x; i < kWarps * E; i += kThreads) wh[i] = 0;
@@ -285,7 +287,7 @@ int launch_counting_sort(bool ep, const int32_t* idx, long long TK, int E, int R
   int rc;
   {
     ProfScope prof(ep ? "ep_hist" : "perm_hist", st);
-    rc = launch_pdl(hist_kernel, NC, kThreads, sh_hist, st, 1, idx, E, g, hist);
+    rc = launch_pdl(hist_kernel, NC, kThreads, sh_hist, st, 1, idx, E, g, hist, ws);
   }
   if (rc) return rc;
   ProfScope prof(ep ? "ep_scatter" : "perm_scatter", st);
@@ -492,7 +494,8 @@ extern "C" int moe_build_permutation_static(const int32_t* topk_idx, int T, int 
   EpOut eo{};
   {
     ProfScope prof("perm_hist", st);
-    rc = launch_pdl(hist_kernel, NC, kThreads, sh_hist, st, 1, topk_idx, E, g, hist);
+    rc = launch_pdl(hist_kernel, NC, kThreads, sh_hist, st, 1, topk_idx, E, g, hist,
+                    static_cast<void*>(nullptr));
   }
   if (rc) return rc;
   ProfScope prof("perm_scatter", st);

@@ -174,8 +174,9 @@ constexpr int kLbBlocks = 256;
 template <int V>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 load_balance_partial_kernel(const float* __restrict__ logits, int T, int E,
-                            float* __restrict__ partial) {
+                            float* __restrict__ partial, void* ws) {
   pdl_enter();
+  if (blockIdx.x == 0 && threadIdx.x == 0) end_backward_record(ws);
   __shared__ float sums[kWarpsPerBlock][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[V];
@@ -328,14 +329,15 @@ load_balance_backward_kernel(const float* __restrict__ logits, const float* __re
 template <int V>
 struct LbLauncher {
   static int run(const float* logits, const int32_t* counts, int T, int E, int K, float* frac,
-                 float* pmean, float* stats, float* partial, cudaStream_t st) {
+                 float* pmean, float* stats, void* ws, cudaStream_t st) {
+    float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspaceHeader);
     const int nblk = static_cast<int>(
         std::min<long long>(kLbBlocks, (static_cast<long long>(T) + kWarpsPerBlock - 1) / kWarpsPerBlock));
     int rc;
     {
       ProfScope prof("load_balance", st);
       rc = launch_pdl(load_balance_partial_kernel<V>, nblk, kWarpsPerBlock * 32, 0, st, 1, logits,
-                      T, E, partial);
+                      T, E, partial, ws);
     }
     if (rc) return rc;
     ProfScope prof("load_balance_final", st);
@@ -452,8 +454,7 @@ extern "C" int moe_load_balance(const float* logits, const int32_t* counts, int 
       !aligned16(stats))
     return MOE_ERR_MISALIGNED;
   if (!ws || !aligned16(ws) || ws_bytes < load_balance_workspace(E)) return MOE_ERR_WORKSPACE;
-  float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspaceHeader);
-  return dispatch_v<LbLauncher>(E, logits, counts, T, E, K, load_frac, prob_mean, stats, partial,
+  return dispatch_v<LbLauncher>(E, logits, counts, T, E, K, load_frac, prob_mean, stats, ws,
                                 as_stream(stream));
 }
 

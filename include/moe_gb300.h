@@ -321,7 +321,11 @@ int moe_grouped_ffn_backward(const moe_bf16* dy, const moe_bf16* xp, const moe_b
  *   part ran on this workspace, or it ran for other sizes or offsets), write
  *   nothing and set the status word to MOE_ERR_DEVICE_CHECK (read it with
  *   moe_read_device_status). The record does not see a change of the
- *   contents of offsets, dy, xp or h between the parts. */
+ *   contents of offsets, dy, xp or h between the parts. Work in between may
+ *   use the same ws for its header alone (moe_grouped_ffn, moe_grouped_gemm and
+ *   others whose workspace is 256 bytes); an operation that writes past the
+ *   header of ws ends the record, and the weight part then reports
+ *   MOE_ERR_DEVICE_CHECK as above. */
 int moe_grouped_ffn_backward_data(const moe_bf16* dy, const moe_bf16* xp, const moe_bf16* gu,
                                   const moe_bf16* h, const int32_t* offsets, int E, int M, int d,
                                   int I, const moe_bf16* w_gate, const moe_bf16* w_up,
