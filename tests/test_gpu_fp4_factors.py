@@ -43,17 +43,18 @@ def _unit_rows(y, want):
 
 
 def _product(rng, ex, g, zero=()):
-    """Rows of size 2^ex times matrices of factors g: (y, float64 result)."""
+    """Rows of size 2^ex times matrices of factors g: (y, float64 result: the factor times the sum)."""
     E, K, N, n = len(g), 192, 136, 40
     offsets = np.arange(E + 1) * n
     x = O.round_bf16(rng.normal(size=(E * n, K)) * np.exp2(ex))
-    val, codes, byte, scale = _matrix(rng, E, N, K, g, zero)
-    off = to_dev(offsets, I32)
+    val, codes, byte, _ = _matrix(rng, E, N, K, np.ones(E), zero)
+    off, g = to_dev(offsets, I32), np.asarray(g, dtype=np.float32)
     rows = B.moe_fp4_quantize_rows(to_dev(x, BF), off)
-    y = f64(B.moe_grouped_gemm_fp4(rows, off, (codes, B.moe_fp4_pack_scales(byte), scale)))
+    y = f64(B.moe_grouped_gemm_fp4(rows, off, (codes, B.moe_fp4_pack_scales(byte), to_dev(g, F32))))
     xv = F.restore(*F.quantize_rows(x, 16), 16)
+    sums = F.grouped_product(xv, offsets, np.swapaxes(val, 1, 2))
     with np.errstate(invalid="ignore"):
-        return y, F.grouped_product(xv, offsets, np.swapaxes(val, 1, 2))
+        return y, np.repeat(g.astype(np.float64), n)[:, None] * sums
 
 
 @pytest.mark.parametrize("ex,g", [
@@ -121,9 +122,9 @@ def test_experts(I, hidden):
 
 
 def test_factors_that_are_not_finite_or_zero():
-    """A matrix factor of zero gives zeros, of Inf or NaN no number where the sum is not zero."""
+    """A matrix factor of zero gives zeros, of Inf Inf by the sum's sign, of NaN NaN."""
     rng = np.random.default_rng(5)
     y, want = _product(rng, 0, [0.0, np.inf, np.nan, 1.0])
     assert (y[:40] == 0).all() and np.isnan(y[80:120]).all()
-    assert np.array_equal(np.isinf(y[40:80]), np.isinf(want[40:80]))
+    assert np.array_equal(y[40:80], want[40:80], equal_nan=True)
     assert np.isfinite(y[120:]).all()
