@@ -554,7 +554,7 @@ extern "C" int moe_fp4_quantize_rows(const moe_bf16* x, const int32_t* inv_perm,
   using namespace moe;
   if (T < 0 || K < 1 || K > 32 || E < 1 || E > 1024 || d < 64 || d % 64 || (block != 16 && block != 32))
     return MOE_ERR_INVALID_ARG;
-  if (!inv_perm && K != 1) return MOE_ERR_INVALID_ARG;
+  if (!inv_perm && K != 1 && T > 0) return MOE_ERR_INVALID_ARG;   // (an empty array may be null)
   const long long M = static_cast<long long>(T) * K;
   if (d > 16384 || M > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
