@@ -208,8 +208,8 @@ def profile_case(which: str):
              "w_down": rnd(E, I, d, sc=0.02)}
         w4 = BL.fp4_weights(w)
         h_scale = torch.full((E,), 8.0 / 2688, device=dev)
-        flops = {"gemm_gate_up_fp4": 4 * M * d * I, "gemm_fp4": 2 * M * d * I,
-                 "gemm_down": 2 * M * d * I, "gemm_wgrad": 2 * M * d * I}
+        flops = {"gemm_gate_up_fp4": 4 * M * d * I, "gemm_down_fp4": 2 * M * d * I,
+                 "gemm_fp4": 2 * M * d * I, "gemm": 2 * M * d * I, "gemm_wgrad": 2 * M * d * I}
         for it in range(2):
             if it == 1:
                 torch.cuda.synchronize()

@@ -495,9 +495,9 @@ pack_scales_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ b,
 
 template <int BLOCK, int TPR, int BPT>
 int launch_rows(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T, int K,
-                int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st) {
+                int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st, const char* name) {
   constexpr int kRows = kThreads / TPR;
-  ProfScope prof("fp4_quantize_rows", st);
+  ProfScope prof(name, st);
   return launch_pdl(quantize_rows_kernel<BLOCK, TPR, BPT>, (static_cast<unsigned>(T) + kRows - 1) / kRows, kThreads,
                     sizeof(int) * 2 * (E + 1), st, 1, static_cast<const uint4*>(x), inv_perm, offsets,
                     E, T, K, M, d, static_cast<uint2*>(q), static_cast<uint32_t*>(sf), row_scale);
@@ -512,8 +512,9 @@ unsigned row_grid(long long rows) {
 
 template <int BLOCK, int BPT>
 int launch_warp_rows(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
-                     int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st) {
-  ProfScope prof("fp4_quantize_rows", st);
+                     int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st,
+                     const char* name) {
+  ProfScope prof(name, st);
   return launch_pdl(quantize_warp_rows_kernel<BLOCK, BPT>, row_grid(T), kThreads,
                     sizeof(int) * 2 * (E + 1), st, 1, static_cast<const uint4*>(x), inv_perm, offsets,
                     E, T, K, M, d, static_cast<uint2*>(q), static_cast<uint32_t*>(sf), row_scale);
@@ -521,28 +522,30 @@ int launch_warp_rows(const void* x, const int32_t* inv_perm, const int32_t* offs
 
 template <int BLOCK>
 int launch_rows_for(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
-                    int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st) {
+                    int K, int M, int d, void* q, void* sf, float* row_scale, cudaStream_t st,
+                    const char* name) {
   const int units = d / 16;
 #define MOE_ROWS(BPT) \
-  return launch_warp_rows<BLOCK, BPT>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st)
+  return launch_warp_rows<BLOCK, BPT>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st, name)
   if (units <= 64) MOE_ROWS(2);
   if (units <= 128) MOE_ROWS(4);
   if (units <= 192) MOE_ROWS(6);
 #undef MOE_ROWS
   if (units <= 256)
-    return launch_rows<BLOCK, 128, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
+    return launch_rows<BLOCK, 128, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st, name);
   if (units <= 512)
-    return launch_rows<BLOCK, kThreads, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
-  return launch_rows<BLOCK, kThreads, 4>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
+    return launch_rows<BLOCK, kThreads, 2>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st,
+                                           name);
+  return launch_rows<BLOCK, kThreads, 4>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st, name);
 }
 
 }  // namespace
 
 int launch_quantize(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
                     int K, int M, int d, int block, void* q, void* sf, float* row_scale,
-                    cudaStream_t st) {
-  return block == 16 ? launch_rows_for<16>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st)
-                     : launch_rows_for<32>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st);
+                    cudaStream_t st, const char* name) {
+  return block == 16 ? launch_rows_for<16>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st, name)
+                     : launch_rows_for<32>(x, inv_perm, offsets, E, T, K, M, d, q, sf, row_scale, st, name);
 }
 
 }  // namespace fp4
@@ -563,7 +566,7 @@ extern "C" int moe_fp4_quantize_rows(const moe_bf16* x, const int32_t* inv_perm,
       (inv_perm && !aligned16(inv_perm)) || (row_scale && !aligned16(row_scale)))
     return MOE_ERR_MISALIGNED;
   return fp4::launch_quantize(x, inv_perm, offsets, E, T, K, static_cast<int>(M), d, block, q, sf,
-                              row_scale, as_stream(stream));
+                              row_scale, as_stream(stream), "fp4_quantize_rows");
 }
 
 extern "C" int moe_fp4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const float* row_scale,

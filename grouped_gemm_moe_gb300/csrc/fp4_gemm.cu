@@ -36,7 +36,7 @@ using namespace gemm;   // PTX helpers, tensor maps
 
 int launch_quantize(const void* x, const int32_t* inv_perm, const int32_t* offsets, int E, int T,
                     int K, int M, int d, int block, void* q, void* sf, float* row_scale,
-                    cudaStream_t st);   // fp4.cu
+                    cudaStream_t st, const char* name);   // fp4.cu
 
 namespace {
 
@@ -615,18 +615,18 @@ constexpr int kDeepMaxE = 448;
 template <int EPI, int BLOCK, int BN, int STAGES, int BOXES, int MAX_E>
 int launch_stages(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
                   const CUtensorMap& tsa, const CUtensorMap& tsb, const CUtensorMap& tc,
-                  const Params& p, long long tiles, cudaStream_t st) {
+                  const Params& p, long long tiles, cudaStream_t st, const char* name) {
   using S = Shape<EPI, BLOCK, BN, STAGES, BOXES>;
   static_assert(S::smem(MAX_E) <= kSmemOptIn, "shared memory");
   static thread_local int configured = -1;
   static thread_local int max_clusters = 0;
   return launch_cluster2(fp4_pair_kernel<EPI, BLOCK, BN, STAGES, BOXES>, kThreads, S::smem(p.E), S::smem(MAX_E),
                          &configured, &max_clusters, tiles,
-                         EPI == OUT ? "gemm_fp4" : "gemm_gate_up_fp4", st, ta, tb0, tb1, tsa, tsb, tc, p);
+                         name, st, ta, tb0, tb1, tsa, tsb, tc, p);
 }
 
 template <int EPI, int BLOCK, int BN>
-int launch_pair(const Operands& o, Params p, cudaStream_t st) {
+int launch_pair(const Operands& o, Params p, cudaStream_t st, const char* name) {
   using S = Shape<EPI, BLOCK, BN, 5, 1>;
   const int per = EPI == OUT ? BN : BN / 2;   // outputs of a tile
   p.n_tiles = (p.N + per - 1) / per;
@@ -648,28 +648,28 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st) {
   const long long mt_upper = (static_cast<long long>(p.M) + BM - 1) / BM + p.E;
   const long long tiles = mt_upper * p.n_tiles;
   if constexpr (EPI != OUT) {
-    return launch_stages<EPI, BLOCK, BN, 5, 1, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
+    return launch_stages<EPI, BLOCK, BN, 5, 1, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
   } else {
     // Up to four k-blocks a tile (K <= 1024) the stores decide, and a second staging box is worth
     // more than a fifth stage: 84 against 90 us at K = 768 (65536 rows, 2048 outputs). Above, the
     // loads do: five stages 141 against 151 us at K = 1408, 799 against 869 at K = 2048.
     if (p.k64 > 16 && p.E <= kDeepMaxE)
-      return launch_stages<EPI, BLOCK, BN, 5, 1, kDeepMaxE>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
-    return launch_stages<EPI, BLOCK, BN, 4, 2, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st);
+      return launch_stages<EPI, BLOCK, BN, 5, 1, kDeepMaxE>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
+    return launch_stages<EPI, BLOCK, BN, 4, 2, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
   }
 }
 
 template <int EPI, int BLOCK>
-int launch_bn(const Operands& o, const Params& p, cudaStream_t st) {
+int launch_bn(const Operands& o, const Params& p, cudaStream_t st, const char* name) {
   // 256 columns a tile even where 128 leave fewer idle (32766 rows of 2048 to 1400, 640 and 384
   // outputs: 64, 42 and 33 us against 76, 44 and 36); gate and up as their scales are laid out
   const bool wide = EPI == OUT ? p.N > 128 : gate_up_half(p.N) == 128;
-  return wide ? launch_pair<EPI, BLOCK, 256>(o, p, st) : launch_pair<EPI, BLOCK, 128>(o, p, st);
+  return wide ? launch_pair<EPI, BLOCK, 256>(o, p, st, name) : launch_pair<EPI, BLOCK, 128>(o, p, st, name);
 }
 
 template <int EPI>
-int launch_block(int block, const Operands& o, const Params& p, cudaStream_t st) {
-  return block == 16 ? launch_bn<EPI, 16>(o, p, st) : launch_bn<EPI, 32>(o, p, st);
+int launch_block(int block, const Operands& o, const Params& p, cudaStream_t st, const char* name) {
+  return block == 16 ? launch_bn<EPI, 16>(o, p, st, name) : launch_bn<EPI, 32>(o, p, st, name);
 }
 
 // The FFN's scratch: H's codes and scale atoms, and for rows scaled by their own maximum H in
@@ -724,7 +724,7 @@ extern "C" int moe_grouped_gemm_fp4(const uint8_t* xq, const uint8_t* xsf, const
   }
   p.out = reinterpret_cast<__nv_bfloat16*>(y);
   p.status = static_cast<int*>(ws);
-  return launch_block<OUT>(block, Operands{xq, w, w, xsf, w_sf, K}, p, as_stream(stream));
+  return launch_block<OUT>(block, Operands{xq, w, w, xsf, w_sf, K}, p, as_stream(stream), "gemm_fp4");
 }
 
 extern "C" int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row_scale,
@@ -779,10 +779,11 @@ extern "C" int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const 
   p.h_atoms = k_atoms(I, block);
   p.status = static_cast<int*>(ws);
   const Operands gu{xq, w_gate, w_up, xsf, wgu_sf, d};
-  int rc = own_rows ? launch_bn<HB, 16>(gu, p, st) : launch_block<H4>(block, gu, p, st);
+  const char* const name = "gemm_gate_up_fp4";
+  int rc = own_rows ? launch_bn<HB, 16>(gu, p, st, name) : launch_block<H4>(block, gu, p, st, name);
   if (rc) return rc;
   if (own_rows) {
-    rc = launch_quantize(p.out, nullptr, offsets, E, M, 1, M, I, block, hq, hsf, hrs, st);
+    rc = launch_quantize(p.out, nullptr, offsets, E, M, 1, M, I, block, hq, hsf, hrs, st, "fp4_quantize_h");
     if (rc) return rc;
   }
   p.N = d;
@@ -791,7 +792,7 @@ extern "C" int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const 
   p.scale1 = h_scale;
   p.h_scale = nullptr;
   p.out = reinterpret_cast<__nv_bfloat16*>(y);
-  return launch_block<OUT>(block, Operands{hq, w_down, w_down, hsf, wd_sf, I}, p, st);
+  return launch_block<OUT>(block, Operands{hq, w_down, w_down, hsf, wd_sf, I}, p, st, "gemm_down_fp4");
 }
 
 namespace moe {

@@ -1306,20 +1306,22 @@ constexpr size_t pair_smem_bytes(int E) {
 }
 
 // Launches the CTA-pair kernel of a forward or input-gradient kind with the
-// shared-memory opt-in sized for the largest expert count it is used with.
+// shared-memory opt-in sized for the largest expert count it is used with. name: the launch's
+// in a profile (null: the kind's in the layer).
 template <int KIND, int BN, int STAGES, bool FP8 = false>
 int launch_pair(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
                 const CUtensorMap& c0, const CUtensorMap& c1, const CUtensorMap& c2,
                 const CUtensorMap& s, const Params& p, long long tiles_upper, int e_max,
-                cudaStream_t st) {
+                cudaStream_t st, const char* name) {
   static thread_local int configured = -1;
   static thread_local int max_clusters = 0;
-  static const char* kNames[] = {"gemm_gate_up", "gemm_down", "gemm_dh", "gemm_dx", "", ""};
-  static const char* kNamesFp8[] = {"gemm_gate_up_fp8", "gemm_down_fp8", "", "", "", ""};
+  static const char* kNames[] = {"gemm_gate_up", "gemm_down", "gemm_dh", "gemm_dx"};
+  static const char* kNamesFp8[] = {"gemm_gate_up_fp8", "gemm_down_fp8", "", ""};
+  if (!name) name = FP8 ? kNamesFp8[KIND] : kNames[KIND];
   return launch_cluster2(grouped_gemm_pair_kernel<KIND, BN, STAGES, FP8>, kThreads,
                          pair_smem_bytes<KIND, BN, STAGES, FP8>(p.E),
                          pair_smem_bytes<KIND, BN, STAGES, FP8>(e_max), &configured,
-                         &max_clusters, tiles_upper, FP8 ? kNamesFp8[KIND] : kNames[KIND], st, a,
+                         &max_clusters, tiles_upper, name, st, a,
                          b0, b1, c0, c1, c2, s, p);
 }
 
@@ -1391,7 +1393,7 @@ template <int KIND, int BN, bool FP8 = false>
 int launch_pair_depth(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
                       const CUtensorMap& c0, const CUtensorMap& c1, const CUtensorMap& c2,
                       const CUtensorMap& s, const Params& p, long long tiles_upper,
-                      cudaStream_t st) {
+                      cudaStream_t st, const char* name = nullptr) {
   constexpr int kDeep = pair_stages_deep<KIND, BN>();
   constexpr int kShallow = pair_stages<KIND, BN>();
   constexpr int kDeepMaxE = pair_max_e<KIND, BN, kDeep, FP8>();
@@ -1400,9 +1402,9 @@ int launch_pair_depth(const CUtensorMap& a, const CUtensorMap& b0, const CUtenso
   if constexpr (kDeepMaxE >= 1) {
     if (p.E <= kDeepMaxE)
       return launch_pair<KIND, BN, kDeep, FP8>(a, b0, b1, c0, c1, c2, s, p, tiles_upper,
-                                               kDeepMaxE < 1024 ? kDeepMaxE : 1024, st);
+                                               kDeepMaxE < 1024 ? kDeepMaxE : 1024, st, name);
   }
-  return launch_pair<KIND, BN, kShallow, FP8>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, 1024, st);
+  return launch_pair<KIND, BN, kShallow, FP8>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, 1024, st, name);
 }
 
 // The bf16 kinds: c0..c2 the epilogue's maps (gate/up: H and the G, U halves of
@@ -1411,11 +1413,12 @@ int launch_pair_depth(const CUtensorMap& a, const CUtensorMap& b0, const CUtenso
 template <int KIND>
 int launch_pair_bn(int bn, const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
                    const CUtensorMap& c0, const CUtensorMap& c1, const CUtensorMap& c2,
-                   const CUtensorMap& s, const Params& p, long long tiles_upper, cudaStream_t st) {
+                   const CUtensorMap& s, const Params& p, long long tiles_upper, cudaStream_t st,
+                   const char* name = nullptr) {
 #if MOE_PAIR_BN_MAX >= 256
-  if (bn == 256) return launch_pair_depth<KIND, 256>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, st);
+  if (bn == 256) return launch_pair_depth<KIND, 256>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, st, name);
 #endif
-  return launch_pair_depth<KIND, 128>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, st);
+  return launch_pair_depth<KIND, 128>(a, b0, b1, c0, c1, c2, s, p, tiles_upper, st, name);
 }
 
 // The N width a pair tile uses for an output of n columns: 256 unless 128-wide
@@ -1736,8 +1739,8 @@ extern "C" int moe_grouped_gemm(const moe_bf16* x, const int32_t* offsets, int E
   p.status = static_cast<int*>(ws);
   const long long tiles = ((static_cast<long long>(M) + BM - 1) / BM + E) * p.n_tiles;
   cudaStream_t st = as_stream(stream);
-  return trans ? launch_pair_bn<BWD_DX>(bn, ta, tb, tb, tc, tc, ta, tc, p, tiles, st)
-               : launch_pair_bn<FWD_DOWN>(bn, ta, tb, tb, tc, tc, tc, tc, p, tiles, st);
+  return trans ? launch_pair_bn<BWD_DX>(bn, ta, tb, tb, tc, tc, ta, tc, p, tiles, st, "gemm_trans")
+               : launch_pair_bn<FWD_DOWN>(bn, ta, tb, tb, tc, tc, tc, tc, p, tiles, st, "gemm");
 }
 
 // dW[e] (+)= X_e^T dY_e: the padded straddling steps of X and dY, then the down projection's weight
