@@ -40,6 +40,7 @@ MOE_OP_NORM_BACKWARD = 9
 MOE_OP_GROUPED_FFN_W4 = 10
 MOE_OP_GROUPED_FFN_FP4 = 11
 MOE_OP_GROUPED_GEMM_WGRAD = 12
+MOE_OP_GROUPED_FFN_FP4_FUSED = 13
 
 WORKSPACE_HEADER = 256
 
@@ -1280,6 +1281,11 @@ def moe_grouped_gemm_fp4(rows, offsets: torch.Tensor, w, block: int = 16,
     return out
 
 
+def fp4_ffn_op(block: int, h_scale) -> int:
+    """The operation id that sizes moe_grouped_ffn_fp4's workspace."""
+    return MOE_OP_GROUPED_FFN_FP4 if block == 16 and h_scale is None else MOE_OP_GROUPED_FFN_FP4_FUSED
+
+
 def moe_grouped_ffn_fp4(rows, offsets: torch.Tensor, wgu, wd, block: int = 16,
                         h_scale: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                         out: Optional[torch.Tensor] = None):
@@ -1308,7 +1314,7 @@ def moe_grouped_ffn_fp4(rows, offsets: torch.Tensor, wgu, wd, block: int = 16,
         if block == 32:
             raise ValueError("h_scale goes with block 16")
         _shaped(h_scale, torch.float32, (E,), "h_scale", dev)
-    ws = _need_ws(ws, workspace_size(MOE_OP_GROUPED_FFN_FP4, M, E, 1, 1, d, I) if ws is None else 0,
+    ws = _need_ws(ws, workspace_size(fp4_ffn_op(block, h_scale), M, E, 1, 1, d, I) if ws is None else 0,
                   dev)
     if out is None:
         out = torch.empty(M, d, dtype=torch.bfloat16, device=dev)

@@ -260,14 +260,14 @@ class MoEFp4Block:
         self.y, self.out = e(TK, d, dt=bf), e(T, d, dt=bf)
         self.ws_route = B.new_workspace(B.workspace_size(B.MOE_OP_ROUTE_PERMUTE_EP, T, E, K, 1), dev)
         self.ws_ffn = B.new_workspace(
-            B.workspace_size(B.MOE_OP_GROUPED_FFN_FP4, TK, E, 1, 1, d, I), dev)
+            B.workspace_size(B.fp4_ffn_op(block, h_scale), TK, E, 1, 1, d, I), dev)
         self.shared = "sgu" in w4
         if self.shared:
             Is = w4["sgu"][0].shape[1]
             self.s_offsets = torch.tensor([0, T], dtype=i32, device=dev)
             self.s_rows, self.ys = rows(T, 1), e(T, d, dt=bf)
             self.ws_sffn = B.new_workspace(
-                B.workspace_size(B.MOE_OP_GROUPED_FFN_FP4, T, 1, 1, 1, d, Is), dev)
+                B.workspace_size(B.fp4_ffn_op(block, sh_scale), T, 1, 1, 1, d, Is), dev)
         self.x = None
 
     def norm(self, x: torch.Tensor) -> torch.Tensor:

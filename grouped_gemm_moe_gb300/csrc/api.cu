@@ -12,7 +12,7 @@ size_t ffn_backward_scratch(long long M, int E, int d, int I);   // grouped_gemm
 size_t load_balance_workspace(int E);                       // route.cu
 size_t ffn_fp8_scratch(long long M, int E, int d, int I);   // grouped_gemm.cu
 size_t wgrad_scratch(int E, int K, int N);                   // grouped_gemm.cu
-size_t ffn_fp4_scratch(long long M, int E, int I);           // fp4_gemm.cu
+size_t ffn_fp4_scratch(long long M, int E, int I, bool own_rows);   // fp4_gemm.cu
 size_t route_permute_workspace(long long TK, int E, int R);   // front.cu
 size_t norm_backward_workspace(int T, int d);               // norm.cu
 
@@ -117,8 +117,9 @@ extern "C" size_t moe_workspace_size(int op, int T, int E, int K, int R, int d, 
       if (I < 64 || d < 64 || d % 64 || I % 64) return 0;
       return kWorkspaceHeader;
     case MOE_OP_GROUPED_FFN_FP4:
+    case MOE_OP_GROUPED_FFN_FP4_FUSED:
       if (I < 64 || d < 64 || d % 64 || I % 64) return 0;
-      return kWorkspaceHeader + ffn_fp4_scratch(TK, E, I);
+      return kWorkspaceHeader + ffn_fp4_scratch(TK, E, I, op == MOE_OP_GROUPED_FFN_FP4);
     case MOE_OP_GROUPED_GEMM_WGRAD:
       if (d < 8 || d % 8 || I < 8 || I % 8) return 0;
       return kWorkspaceHeader + wgrad_scratch(E, d, I);

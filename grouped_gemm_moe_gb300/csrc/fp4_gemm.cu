@@ -677,21 +677,23 @@ int launch_block(int block, const Operands& o, const Params& p, cudaStream_t st,
 struct Scratch {
   size_t hq, hsf, h, hrs, total;
 };
-Scratch ffn_layout(long long M, int E, int I) {
+Scratch ffn_layout(long long M, int E, int I, bool own_rows) {
   auto up = [](size_t b) { return (b + 1023) & ~static_cast<size_t>(1023); };
   Scratch s;
   s.hq = 0;
   s.hsf = up(static_cast<size_t>(M) * (I / 2));
   s.h = s.hsf + up(static_cast<size_t>(row_tiles(M, E)) * k_atoms(I, 16) * 512);
-  s.hrs = s.h + up(static_cast<size_t>(M) * I * 2);
-  s.total = s.hrs + up(static_cast<size_t>(M) * 4);
+  s.hrs = s.h + (own_rows ? up(static_cast<size_t>(M) * I * 2) : 0);
+  s.total = s.hrs + (own_rows ? up(static_cast<size_t>(M) * 4) : 0);
   return s;
 }
 
 }  // namespace
 }  // namespace fp4
 
-size_t ffn_fp4_scratch(long long M, int E, int I) { return fp4::ffn_layout(M, E, I).total; }
+size_t ffn_fp4_scratch(long long M, int E, int I, bool own_rows) {
+  return fp4::ffn_layout(M, E, I, own_rows).total;
+}
 
 }  // namespace moe
 
@@ -753,15 +755,15 @@ extern "C" int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const 
         static_cast<const void*>(down_scale), static_cast<const void*>(h_scale),
         static_cast<const void*>(y)})
     if (!aligned16(ptr)) return MOE_ERR_MISALIGNED;
-  const Scratch lay = ffn_layout(M, E, I);
+  const bool own_rows = block == 16 && !h_scale;   // H's rows scaled by their own maximum
+  const Scratch lay = ffn_layout(M, E, I, own_rows);
   if (!ws || !aligned16(ws) || ws_bytes < kWorkspaceHeader + lay.total) return MOE_ERR_WORKSPACE;
   if (cc_major() < 10) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = as_stream(stream);
   uint8_t* scratch = static_cast<uint8_t*>(ws) + kWorkspaceHeader;
   uint8_t* hq = scratch + lay.hq;
   uint8_t* hsf = scratch + lay.hsf;
-  float* hrs = reinterpret_cast<float*>(scratch + lay.hrs);
-  const bool own_rows = block == 16 && !h_scale;   // H's rows scaled by their own maximum
+  float* hrs = reinterpret_cast<float*>(scratch + lay.hrs);   // own_rows, as the bf16 H
   Params p{};
   p.offsets = offsets;
   p.E = E;
@@ -773,7 +775,7 @@ extern "C" int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const 
     p.scale1 = up_scale;
   }
   p.h_scale = h_scale;
-  p.out = reinterpret_cast<__nv_bfloat16*>(scratch + lay.h);
+  p.out = own_rows ? reinterpret_cast<__nv_bfloat16*>(scratch + lay.h) : nullptr;
   p.hq = hq;
   p.hsf = reinterpret_cast<uint32_t*>(hsf);
   p.h_atoms = k_atoms(I, block);

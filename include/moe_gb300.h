@@ -76,7 +76,8 @@ enum moe_op {
   MOE_OP_NORM_BACKWARD = 9,
   MOE_OP_GROUPED_FFN_W4 = 10,
   MOE_OP_GROUPED_FFN_FP4 = 11,
-  MOE_OP_GROUPED_GEMM_WGRAD = 12
+  MOE_OP_GROUPED_GEMM_WGRAD = 12,
+  MOE_OP_GROUPED_FFN_FP4_FUSED = 13
 };
 
 /* Bytes of device workspace the operation needs for these sizes (0 on bad
@@ -756,7 +757,8 @@ int moe_grouped_gemm_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row
  *   w_gate, w_up [E,I,d/2], wgu_sf their scales packed together, gate_scale, up_scale [E];
  *   w_down [E,d,I/2], wd_sf, down_scale [E] (factors not read with block 32).
  *   y [M,d] bf16 out; rows past offsets[E] are not written.
- *   ws: moe_workspace_size(MOE_OP_GROUPED_FFN_FP4, M, E, 1, 1, d, I) bytes.
+ *   ws: moe_workspace_size(MOE_OP_GROUPED_FFN_FP4, M, E, 1, 1, d, I) bytes; with h_scale
+ *   or block 32, where H is never in bf16, MOE_OP_GROUPED_FFN_FP4_FUSED (2 M I bytes less).
  * d % 64 == 0, I % 64 == 0, I <= 16384, E <= 1024. */
 int moe_grouped_ffn_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row_scale,
                         const int32_t* offsets, int E, int M, int d, int I, int block,
