@@ -267,4 +267,20 @@ __device__ __forceinline__ bool index_ok(bool) { return true; }
 #define MOE_DEBUG_STATUS_READER(name)
 #endif
 
+// Debug builds: whether expert offsets s_off [E + 1] start at 0, never decrease and end within M
+// rows, recorded like an index if not. Every thread of the block calls it, after the barrier behind
+// which s_off is written. Release builds: true.
+__device__ __forceinline__ bool offsets_in_order(const int* s_off, int E, int M) {
+#ifdef MOE_DEBUG_CHECKS
+  bool ok = s_off[0] == 0 && s_off[E] <= M;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) ok = ok && s_off[e] <= s_off[e + 1];
+  return index_ok(__syncthreads_and(ok) != 0);
+#else
+  (void)s_off;
+  (void)E;
+  (void)M;
+  return true;
+#endif
+}
+
 }  // namespace moe

@@ -132,6 +132,7 @@ quantize_warp_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict
   pdl_enter();
   for (int e = threadIdx.x; e <= E; e += kThreads) s_off[e] = __ldg(offsets + e);
   __syncthreads();
+  if (!offsets_in_order(s_off, E, M)) return;   // where a row's scales are follows from them
   if (threadIdx.x < 32) tile_prefix(s_off, s_tile, E);
   __syncthreads();
   constexpr int kPer = BLOCK / 4;              // units of a scale word
@@ -236,6 +237,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ in
   }
   for (int e = threadIdx.x; e <= E; e += kThreads) s_off[e] = __ldg(offsets + e);
   __syncthreads();
+  if (!offsets_in_order(s_off, E, M)) return;   // where a row's scales are follows from them
   if (threadIdx.x < 32) tile_prefix(s_off, s_tile, E);
   // the row's largest element, for its factor
   uint32_t top[BPT];
@@ -309,6 +311,7 @@ dequantize_rows_kernel(const uint2* __restrict__ q, const uint32_t* __restrict__
   pdl_enter();
   for (int e = threadIdx.x; e <= E; e += kThreads) s_off[e] = __ldg(offsets + e);
   __syncthreads();
+  if (!offsets_in_order(s_off, E, M)) return;   // where a row's scales are follows from them
   if (threadIdx.x < 32) tile_prefix(s_off, s_tile, E);
   __syncthreads();
   const int lane = threadIdx.x & 31;

@@ -54,6 +54,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ of
   int* s_tile = smq + E + 1;   // [E + 1]: first scale tile of each expert
   for (int e = threadIdx.x; e <= E; e += kQThreads) s_off[e] = __ldg(offsets + e);
   __syncthreads();
+  if (!offsets_in_order(s_off, E, M)) return;   // where a row's scales are follows from them
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     int carry = 0;

@@ -778,9 +778,10 @@ int moe_debug_wait_timeout(void* ws, int timeout_us, void* stream);
 /* Debug builds only (compiled with -DMOE_DEBUG_CHECKS; the package builds
  * them as libmoe_gb300_debug.so): every gathered or scattered index (perm,
  * inv_perm, the expert ids the permutation sorts, the regroup indices) is
- * range-checked before its access, and the grouped GEMMs check their expert
- * offsets (non-decreasing from 0, ending within M; on failure they also set the
- * workspace status word and compute nothing). A failed check skips the access
+ * range-checked before its access, and the grouped GEMMs and the quantizers
+ * that lay scales out by expert check their expert offsets (non-decreasing from 0,
+ * ending within M; on failure they compute nothing, and the GEMMs also set the
+ * workspace status word). A failed check skips the access
  * (or redirects a read to row 0) and records MOE_ERR_DEVICE_CHECK. This call
  * synchronises the device, stores the first recorded code (0 if none) in
  * *host_status and clears the record. Release builds return
