@@ -747,7 +747,7 @@ int moe_grouped_gemm_fp4(const uint8_t* xq, const uint8_t* xsf, const float* row
 
 /* Grouped SwiGLU experts on 4-bit activations and weights, forward: G, U the products with
  * w_gate and w_up, H = silu(G) U, y = bf16(quantized H times w_down). H is quantized
- *   block 16, h_scale [E] fp32 given: with g = h_scale[e] (2^-100 to 2^100, from a calibration
+ *   block 16, h_scale [E] fp32 given: with g = h_scale[e] (2^-100 to 2^117, from a calibration
  *     run: about its largest |H| / 2688), larger values saturating at 2688 h_scale[e]; fp32 H,
  *     one pass;
  *   block 16, h_scale NULL: H rounded to bf16, then as moe_fp4_quantize_rows does (its rows

@@ -128,3 +128,28 @@ def test_factors_that_are_not_finite_or_zero():
     assert (y[:40] == 0).all() and np.isnan(y[80:120]).all()
     assert np.array_equal(y[40:80], want[40:80], equal_nan=True)
     assert np.isfinite(y[120:]).all()
+
+
+@pytest.mark.parametrize("ex", [-92, 0, 105, 121])
+def test_hidden_factors_at_their_ends(ex):
+    """H of size 2^ex under a fixed factor of 2^-99 to 2^115."""
+    rng = np.random.default_rng([ex + 200, 3])
+    E, d, I, n = 3, 192, 192, 70
+    offsets = np.arange(E + 1) * n
+    x = O.round_bf16(rng.normal(size=(E * n, d)))
+    unit = np.array([1.3, 0.9, 1.6], dtype=np.float32)
+    wg, gq, gs, gg = _matrix(rng, E, I, d, unit * 2.0 ** -12)
+    wu, uq, us, ug = _matrix(rng, E, I, d, unit * 2.0 ** (ex - 12))
+    wd, dq, ds, dg = _matrix(rng, E, d, I, unit * 2.0 ** -ex)
+    xv = F.restore(*F.quantize_rows(x, 16), 16)
+    t = lambda w: np.swapaxes(w, 1, 2)   # noqa: E731
+    h = F.swiglu(F.grouped_product(xv, offsets, t(wg)), F.grouped_product(xv, offsets, t(wu)))
+    hs = (np.abs(h).reshape(E, -1).max(1) / 2688).astype(np.float32)
+    assert (hs >= 2.0 ** -100).all() and (hs <= 2.0 ** 117).all()
+    off = to_dev(offsets, I32)
+    y = f64(B.moe_grouped_ffn_fp4(B.moe_fp4_quantize_rows(to_dev(x, BF), off), off,
+                                  (gq, uq, B.moe_fp4_pack_scales(gs, us), gg, ug),
+                                  (dq, B.moe_fp4_pack_scales(ds), dg), h_scale=to_dev(hs, F32)))
+    want, _ = F.grouped_ffn_fp4(xv, offsets, wg, wu, wd, 16, h_scale=hs.astype(np.float64))
+    off_rows = (rounding_excess(y, want) > 1e-3 * np.sqrt(np.mean(want ** 2))).any(1)
+    assert off_rows.sum() <= 3, off_rows.sum()      # E n I 2^-16 = 0.6 rows with a changed code
