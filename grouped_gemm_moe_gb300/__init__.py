@@ -5,8 +5,9 @@ tree by ``grouped_gemm_moe_gb300.build.build()``. ``binding`` exposes each C
 entry point under its own name for torch tensors; ``layer.MoELayer`` runs a
 whole layer's forward and backward as a sequence of those calls, in bf16 or on
 8-bit activation checkpoints; ``block`` puts the norms, the gate and the
-residual around it for training, and runs the block on 4-bit experts for
-decoding; ``workloads`` draws the seeded synthetic inputs.
+residual around it for training, runs the block on 4-bit experts for
+decoding and on microscaled 4-bit floats, activations included, for prefill;
+``workloads`` draws the seeded synthetic inputs.
 
 Importing the package does not load the library; the first binding call
 does, and raises if it has not been built.

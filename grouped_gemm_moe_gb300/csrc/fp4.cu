@@ -118,8 +118,11 @@ __device__ __forceinline__ uint2 encode_unit(const uint4& a, const uint4& b, uin
 // CTA. The lanes look the K destinations up side by side, and the scale words, each in a
 // sector of its own, are spread over the lanes before they are stored. Those words are what
 // keeps wide copies from HBM speed: 32768 x 4096 to 8 experts takes 191 us (floor 129), 134
-// without them. Block 16, rows of 2112 to 6: 27 us, a CTA of 128 threads a row 32; rows of 1408
-// to one: 77 us, 64 threads a row 93; rows of 4096 to 8: 220 us, 128 threads a row 191.
+// without them. Block 16, a warp a row against a CTA of 128 threads a row: 65536 rows to one, 2112 columns
+// 72 and 117 us, 2560 79 and 117, 2944 90 and 119, 3584 110 and 122; 16384 to 6, 48 and 55, 56 and
+// 56, 63 and 60, 74 and 70; to 8, 59 and 62, 71 and 66, 84 and 74, 94 and 87 (32768 rows of 4096
+// to 8: 220 and 191). The crossing lies lower the more copies a row has; 192 units stand for all.
+// 98304 rows of 1408 to one: 77 us, 64 threads a row 93.
 template <int BLOCK, int BPT>
 __global__ void __launch_bounds__(kThreads)
 quantize_warp_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ inv_perm,

@@ -18,10 +18,14 @@
 //   * one 256 x BN accumulator: eight epilogue warps take it into registers at once (128
 //     columns a thread) and hand it back before they work on it, so the next tile's MMAs wait
 //     for the TMEM loads only. (Two accumulators of 256 columns leave no TMEM for scales.)
-//     With no loads a tile of 16 k-blocks takes 5.0 us, 0.6 of them the handover; the drafter
-//     workload's gate and up (262144 rows, d 4096, I 2048) 1.12 ms so and 1.28 ms in earnest,
-//     6.9 PFLOP/s; its down projection 0.63 and 0.80 ms. The difference is operands in flight:
-//     38 KB per k-block and CTA, five stages of them;
+//     The drafter workload's gate and up (262144 rows, d 4096, I 2048): 1.28 ms, 6.9 PFLOP/s.
+//     Parts by themselves: MMAs and copies of scales 1.03 ms (8.6 PFLOP/s, the rate of steps of
+//     64 K), loads 0.94, both together without the epilogue's work 1.16, MMAs with the epilogue
+//     1.13. Its down projection: 0.79 ms, MMAs 0.56, loads 0.46, both 0.60; there the epilogue's
+//     bf16 stores count for most (loads and epilogue without MMAs 0.67). So no single part binds:
+//     MMAs and loads take nearly as long as each other and slow each other by a seventh, and a
+//     tile's epilogue is hidden in part (one accumulator). sm_103a also has steps of 96 K, which
+//     these kernels do not use;
 //   * the MMA thread is elected (elect_one): with a branch on the lane number the same gate and
 //     up took 3.6 ms;
 //   * the SwiGLU epilogue quantizes H in registers: codes and scale words leave directly, and
@@ -651,8 +655,9 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st, const char* name) 
     return launch_stages<EPI, BLOCK, BN, 5, 1, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
   } else {
     // Up to four k-blocks a tile (K <= 1024) the stores decide, and a second staging box is worth
-    // more than a fifth stage: 84 against 90 us at K = 768 (65536 rows, 2048 outputs). Above, the
-    // loads do: five stages 141 against 151 us at K = 1408, 799 against 869 at K = 2048.
+    // as much as a fifth stage or more; above, the loads do. 65536 rows, 2048 outputs, two boxes
+    // against five stages: K = 512 70 and 72 us, 768 74 and 76, 896 to 1024 79 both, 1088 94 and
+    // 85, 1280 99 and 85, 1408 107 and 97; 16 experts, 32768 rows, 4096 outputs cross there too.
     if (p.k64 > 16 && p.E <= kDeepMaxE)
       return launch_stages<EPI, BLOCK, BN, 5, 1, kDeepMaxE>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
     return launch_stages<EPI, BLOCK, BN, 4, 2, 1024>(ta, tb0, tb1, tsa, tsb, tc, p, tiles, st, name);
@@ -662,7 +667,9 @@ int launch_pair(const Operands& o, Params p, cudaStream_t st, const char* name) 
 template <int EPI, int BLOCK>
 int launch_bn(const Operands& o, const Params& p, cudaStream_t st, const char* name) {
   // 256 columns a tile even where 128 leave fewer idle (32766 rows of 2048 to 1400, 640 and 384
-  // outputs: 64, 42 and 33 us against 76, 44 and 36); gate and up as their scales are laid out
+  // outputs: 64, 42 and 33 us against 76, 44 and 36). Gate and up as their scales are laid out:
+  // 64 + 64 columns where I is 64 more than a multiple of 128; 128 + 128 with a last tile half
+  // idle would need another layout of the packed scales and has not been timed.
   const bool wide = EPI == OUT ? p.N > 128 : gate_up_half(p.N) == 128;
   return wide ? launch_pair<EPI, BLOCK, 256>(o, p, st, name) : launch_pair<EPI, BLOCK, 128>(o, p, st, name);
 }

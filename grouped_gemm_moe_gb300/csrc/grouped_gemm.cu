@@ -10,7 +10,10 @@
 // the FSDP2 backend" names a grouped_mm backend over expert-sorted rows; that
 // is prior art, this is an independent kernel.
 //
-// Kernel shape (two templates, six problem kinds, all on CTA pairs):
+// The products by themselves (moe_grouped_gemm, as stored or transposed, and
+// moe_grouped_gemm_wgrad) run on the same templates.
+//
+// Kernel shape (two templates, seven problem kinds, all on CTA pairs):
 //   * every GEMM runs on clusters of two CTAs sharing one tcgen05 MMA of
 //     M = 256 (cta_group::2): each CTA stages its 128 rows of A and half of
 //     B's N, the leader issues the MMA, and each CTA's TMEM holds its own 128

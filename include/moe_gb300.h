@@ -676,6 +676,7 @@ int moe_grouped_gemm(const moe_bf16* x, const int32_t* offsets, int E, int M, in
 
 /* Its weight gradient: dw[e] = x_e^T dy_e (fp32), or dw[e] += with accumulate != 0 (the
  * sum of one call is added once to each element, so results are the same bits on every run).
+ * The sums are the tensor cores' in fp32: off by a few 1e-7 of dw's size at 500 rows an expert.
  *   x [M,K], dy [M,N] bf16 in; dw [E,K,N] fp32. Experts without rows: zero, or unchanged.
  *   An expert's dw depends on its own rows alone (an Inf or NaN in others' stays there).
  *   ws: moe_workspace_size(MOE_OP_GROUPED_GEMM_WGRAD, M, E, 1, 1, K, N) bytes. */
@@ -709,7 +710,8 @@ int moe_grouped_gemm_wgrad(const moe_bf16* x, const moe_bf16* dy, const int32_t*
  *   x [T,d] bf16, inv_perm [T*K] int32, offsets [E+1] int32 in.
  *   q [T*K, d/2] uint8, sf [tiles, KA, 512] uint8 (tiles for M = T*K), row_scale [T*K] fp32
  *   (block 16; NULL with block 32) out. Scales of rows past an expert's last row are not
- *   written (rows past offsets[E] get codes and a factor alone, which no product reads). 64 <= d <= 16384, K <= 32, E <= 1024. */
+ *   written (rows past offsets[E] get codes and a factor alone, which no product reads).
+ *   64 <= d <= 16384, K <= 32, E <= 1024. */
 int moe_fp4_quantize_rows(const moe_bf16* x, const int32_t* inv_perm, int T, int K,
                           const int32_t* offsets, int E, int d, int block, uint8_t* q, uint8_t* sf,
                           float* row_scale, void* stream);
