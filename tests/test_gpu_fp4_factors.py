@@ -42,9 +42,9 @@ def _unit_rows(y, want):
     return y / size, want / size
 
 
-def _product(rng, ex, g, zero=()):
+def _product(rng, ex, g, zero=(), N=136, K=192):
     """Rows of size 2^ex times matrices of factors g: (y, float64 result: the factor times the sum)."""
-    E, K, N, n = len(g), 192, 136, 40
+    E, n = len(g), 40
     offsets = np.arange(E + 1) * n
     x = O.round_bf16(rng.normal(size=(E * n, K)) * np.exp2(ex))
     val, codes, byte, _ = _matrix(rng, E, N, K, np.ones(E), zero)
@@ -57,14 +57,15 @@ def _product(rng, ex, g, zero=()):
         return y, np.repeat(g.astype(np.float64), n)[:, None] * sums
 
 
+@pytest.mark.parametrize("N,K", [(136, 192), (72, 192), (136, 1152)])     # every instance of the product
 @pytest.mark.parametrize("ex,g", [
     (-70, 1.36 * 2.0 ** -64),    # factors 2^-80 2^-64: a subnormal product of five bits, sums of 2^21
     (-90, 1.36 * 2.0 ** -44),    # the same, rows smaller
     (-88, 1.9 * 2.0 ** -100),    # the result is zero
     (60, 1.1 * 2.0 ** -70), (-60, 1.1 * 2.0 ** 60), (-80, 1.7 * 2.0 ** 100), (100, 1.7 * 2.0 ** -100),
 ])
-def test_product(ex, g):
-    y, want = _product(np.random.default_rng([ex + 200, 1]), ex, [g, g * 1.7, g * 2.5])
+def test_product(ex, g, N, K):
+    y, want = _product(np.random.default_rng([ex + 200, 1]), ex, [g, g * 1.7, g * 2.5], N=N, K=K)
     if np.abs(want).max() < 2.0 ** -135:      # below half the smallest bf16
         assert (y == 0).all()
         return
